@@ -450,6 +450,141 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
                               int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Single-exit LM-head operators                                             */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * What the multi-exit loss has for a suite at hand, these have for one exit's
+ * hidden states h [T, D] and head W [V, D] alone: log probabilities of given
+ * tokens (scoring, decoding, policy gradients), and distillation from a
+ * teacher of which only its top logits were kept.  The pages have no
+ * counterpart.  Logits are l = W h, q = softmax(l), lse = log sum_v e^l_v.
+ *
+ * Common arguments
+ *   T, D, V    tokens, width, vocabulary.  MLS_BF16 needs D % 64 == 0; V is
+ *              any size.  MLS_F32 accepts any sizes (CUDA-core path).
+ *   h, W       device dt [T, D] and dt [V, D], 16-byte aligned
+ *   ids        device int32; -1 means "no token there" (its outputs are 0, it
+ *              has no gradient); any other value outside [0, V) is treated the
+ *              same and sets MLS_DEVFLAG_BAD_ID
+ *   dh         device dt [T, D], overwritten, or NULL
+ *   dW         device [V, D] of dW_dt, or NULL (a frozen head): MLS_F32, added
+ *              to with accumulate_dW != 0, or (with MLS_BF16 inputs) MLS_BF16,
+ *              rounded once from the fp32 sum; MLS_BF16 with accumulate_dW is
+ *              MLS_ERR_UNSUPPORTED.  dh and dW must not both be NULL.
+ *   workspace  device, 16-byte aligned.  The queries give the size that works
+ *              in one piece, or within 1.5 GiB in pieces; any size of at least
+ *              the minimum (each min pointer may be NULL) is accepted, and a
+ *              smaller one means more pieces.  Nothing in it is kept from call
+ *              to call; two calls that may overlap on the GPU (two captured
+ *              graphs among them) need one each.
+ * Results are deterministic for a given workspace size (no floating-point
+ * atomics).
+ */
+
+/*
+ * mls_token_logprobs
+ *   N          given tokens per position, 0 <= N <= 64 (ids and logp may be
+ *              NULL when N = 0)
+ *   logp       device f32 [T, N]: l[t, ids[t, n]] - lse_t
+ *   stats      device f32 [2, T]: lse_t, and the entropy -sum_v q log q
+ *   K          alternatives per position, 0 <= K <= min(64, V), V <= 2^21 with
+ *              K > 0; N + K >= 1
+ *   top_ids    device int32 [T, K]: the K largest logits, largest first, equal
+ *              ones by ascending id.  The order is that of the products summed
+ *              in 64 bits, so it does not depend on T, the workspace or the
+ *              position.  -1 where fewer than K logits are numbers.
+ *   top_logp   device f32 [T, K]: their log probabilities
+ * Without alternatives MLS_BF16 never writes the logits; with them, the logits
+ * of one block of tokens at a time go to the workspace in fp32.
+ */
+mls_status mls_token_logprobs_workspace(int64_t T, int64_t D, int64_t V, int N, int K, mls_dtype dt,
+                                        size_t* bytes, size_t* min_bytes);
+
+mls_status mls_token_logprobs(int64_t T, int64_t D, int64_t V, int N, const int32_t* ids,
+                              const void* h, const void* W, mls_dtype dt,
+                              float* logp, float* stats,
+                              int K, int32_t* top_ids, float* top_logp,
+                              void* workspace, size_t ws_bytes,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * mls_token_logprobs_bwd -- with g = dL/dlogp and e = dL/dentropy,
+ *   dL/dl_v = -q_v (sum_n g_n + e (log q_v + entropy)) + sum over ids_n = v of g_n
+ *   dh = dL/dl W,  dW (+)= dL/dl^T h
+ *   stats      the forward call's, for the same h and W
+ *   g_logp     device f32 [T, N], 1 <= N <= 64 (entries without a token are not read as gradients)
+ *   g_entropy  device f32 [T] or NULL (0)
+ * The alternatives are given tokens too: pass their ids and gradients.
+ * MLS_BF16: dL/dl is formed in fp16 (11-bit significand, each row over a power
+ * of two near its largest coefficient) for one chunk of the vocabulary at a
+ * time, and multiplied on the tensor cores with fp16 copies of W and h, fp32
+ * sums.
+ */
+mls_status mls_token_logprobs_bwd_workspace(int64_t T, int64_t D, int64_t V, int N, mls_dtype dt,
+                                            size_t* bytes, size_t* min_bytes);
+
+mls_status mls_token_logprobs_bwd(int64_t T, int64_t D, int64_t V, int N, const int32_t* ids,
+                                  const void* h, const void* W, mls_dtype dt,
+                                  const float* stats, const float* g_logp, const float* g_entropy,
+                                  void* dh, void* dW, mls_dtype dW_dt, int accumulate_dW,
+                                  void* workspace, size_t ws_bytes,
+                                  int32_t* dev_status, void* stream);
+
+/*
+ * mls_topk_distill_fwd -- next-token cross-entropy mixed with the
+ * cross-entropy to a teacher's top logits.  With p_t = softmax over the K
+ * teacher logits present at token t (mls_token_logprobs writes such lists):
+ *   CE_t = lse_t - l_t,y_t
+ *   KD_t = sum_k p_t,k (lse_t - l_t,ids_k)       (0 where no teacher token is present)
+ *   losses[0] = 1/T sum_t w_t CE_t, losses[1] = 1/T sum_t w_t KD_t,
+ *   losses[2] = (1 - alpha_d) losses[0] + alpha_d losses[1]
+ *   K               teacher tokens per position, 1 <= K <= 64
+ *   teacher_ids     device int32 [T, K], -1 for absent ones; an id that occurs
+ *                   twice counts with the sum of its probabilities
+ *   teacher_logits  device f32 [T, K]: logits or log probabilities (a constant
+ *                   per token does not matter), finite or -infinity; those of
+ *                   absent tokens are not read as numbers.  A token whose
+ *                   logits are all -infinity has no teacher.
+ *   token_weights   device f32 [T] or NULL (1); a token of weight 0 (padding)
+ *                   counts in no loss and no gradient, whatever its target
+ *                   and rows hold
+ *   y_targets       device int32 [T]; a target outside [0, V) at a weight
+ *                   other than 0 sets MLS_DEVFLAG_BAD_ID and the token has
+ *                   weight 0
+ *   losses          device f32 [3]
+ *   stats           device f32 [3, T]: lse_t, CE_t, KD_t (the last two 0 where
+ *                   the target is outside [0, V))
+ * A non-finite alpha_d is MLS_ERR_INVALID_ARG.
+ */
+mls_status mls_topk_distill_workspace(int64_t T, int64_t D, int64_t V, int K, mls_dtype dt,
+                                      size_t* fwd_bytes, size_t* fwd_min, size_t* bwd_bytes, size_t* bwd_min);
+
+mls_status mls_topk_distill_fwd(int64_t T, int64_t D, int64_t V, int K,
+                                const int32_t* y_targets, const int32_t* teacher_ids,
+                                const float* teacher_logits, const float* token_weights,
+                                const void* h, const void* W, float alpha_d, mls_dtype dt,
+                                float* losses, float* stats,
+                                void* workspace, size_t ws_bytes,
+                                int32_t* dev_status, void* stream);
+
+/*
+ * mls_topk_distill_bwd -- gradients of losses[2] times grad_scale (finite):
+ *   dL/dl_v = w_t grad_scale / T ( q_v ((1 - alpha_d) + alpha_d [any teacher token])
+ *             - (1 - alpha_d) [v = y_t] - alpha_d sum over ids_k = v of p_k )
+ *   dh = dL/dl W,  dW (+)= dL/dl^T h,  formed as in mls_token_logprobs_bwd
+ * stats: the forward call's (its lse row is read).  The teacher gets no gradient.
+ */
+mls_status mls_topk_distill_bwd(int64_t T, int64_t D, int64_t V, int K,
+                                const int32_t* y_targets, const int32_t* teacher_ids,
+                                const float* teacher_logits, const float* token_weights,
+                                const void* h, const void* W, float alpha_d, mls_dtype dt,
+                                const float* stats, float grad_scale,
+                                void* dh, void* dW, mls_dtype dW_dt, int accumulate_dW,
+                                void* workspace, size_t ws_bytes,
+                                int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                    */
 /* ------------------------------------------------------------------------ */
 

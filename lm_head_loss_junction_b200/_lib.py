@@ -78,6 +78,20 @@ PROTOTYPES = {
     "mls_exit_agreement_workspace": (_int, [_int, _i64, ctypes.POINTER(_i64), _i64, _int, ctypes.POINTER(_sz)]),
     "mls_exit_agreement": (_int, [_int, _i64, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                   _int, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "mls_token_logprobs_workspace": (_int, [_i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(_sz),
+                                            ctypes.POINTER(_sz)]),
+    "mls_token_logprobs": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp, _int, _vp, _vp,
+                                  _vp, _sz, _vp, _vp]),
+    "mls_token_logprobs_bwd_workspace": (_int, [_i64, _i64, _i64, _int, _int, ctypes.POINTER(_sz),
+                                                ctypes.POINTER(_sz)]),
+    "mls_token_logprobs_bwd": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp, _int,
+                                      _int, _vp, _sz, _vp, _vp]),
+    "mls_topk_distill_workspace": (_int, [_i64, _i64, _i64, _int, _int, ctypes.POINTER(_sz), ctypes.POINTER(_sz),
+                                          ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "mls_topk_distill_fwd": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _int, _vp, _vp,
+                                    _vp, _sz, _vp, _vp]),
+    "mls_topk_distill_bwd": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _int, _vp, _f32,
+                                    _vp, _vp, _int, _int, _vp, _sz, _vp, _vp]),
     "mls_selftest_wait_timeout": (_int, [_int, _i64, _i64, ctypes.POINTER(_i64), _vp, ctypes.POINTER(_vp),
                                          ctypes.POINTER(_vp), _vp, _vp, _vp, _sz, ctypes.c_uint64, _vp, _vp]),
     "mls_status_read": (_int, [_vp, _vp, ctypes.POINTER(_i32)]),

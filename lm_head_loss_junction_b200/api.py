@@ -320,6 +320,215 @@ def exit_agreement(h: List[torch.Tensor], W: List[torch.Tensor], stats: torch.Te
     return metrics, rows, top1
 
 
+# ---------------------------------------------------------------- single-exit LM-head operators
+def _head_common(h, W):
+    _need(h, "h", ndim=2)
+    _need(W, "W", h.dtype, 2)
+    if h.shape[1] != W.shape[1]:
+        raise ValueError("h must be [T, D] and W [V, D]")
+    if W.device != h.device:
+        raise ValueError("W must be on the device of h")
+    return h.shape[0], h.shape[1], W.shape[0], _dtype_code(h)
+
+
+def _same_device(h, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != h.device:
+            raise ValueError(f"{name} must be on the device of h")
+
+
+def _head_rows(t, name, dtype, shape):
+    """t as given, or None; checked to be contiguous, of the dtype and the shape."""
+    if t is None:
+        return None
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _head_workspace(ws, nbytes, h):
+    if ws is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=h.device), nbytes
+    _need(ws, "workspace")
+    _same_device(h, workspace=ws)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW):
+    if not want_dh and dh is not None or not want_dW and dW is not None:
+        raise ValueError("an output was given for a gradient that is not wanted")
+    if want_dh and dh is None:
+        dh = torch.empty_like(h)
+    if want_dW and dW is None:
+        if accumulate_dW:
+            raise ValueError("accumulate_dW needs dW")
+        dW = torch.empty(W.shape, dtype=dW_dtype, device=W.device)
+    dh = _head_rows(dh, "dh", h.dtype, h.shape)
+    dW = _head_rows(dW, "dW", dW.dtype if dW is not None else None, W.shape)
+    _same_device(h, dh=dh, dW=dW)
+    return dh, dW, _dtype_code(dW) if dW is not None else MLS_F32
+
+
+def token_logprobs_workspace(T: int, D: int, V: int, N: int, top_k: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """(bytes, smallest accepted bytes) of token_logprobs (see mls_token_logprobs_workspace)."""
+    n, least = ctypes.c_size_t(), ctypes.c_size_t()
+    check("mls_token_logprobs_workspace",
+          lib().mls_token_logprobs_workspace(T, D, V, N, top_k, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
+                                             ctypes.byref(n), ctypes.byref(least)))
+    return n.value, least.value
+
+
+def token_logprobs(ids: Optional[torch.Tensor], h: torch.Tensor, W: torch.Tensor, *, top_k: int = 0, logp=None,
+                   stats=None, top_ids=None, top_logp=None, workspace=None, status=None, stream=None):
+    """Log probabilities of given tokens under softmax(h W^T), the entropy of that distribution and its top
+    alternatives, without writing the logits out (see mls_token_logprobs).
+
+    ids: int32 [T] or [T, N] (-1: no token there), or None with top_k > 0.  Returns (logp of the shape of ids or
+    None, stats [2, T] = log-sum-exp and entropy, top_ids [T, top_k] or None, top_logp [T, top_k] or None).
+    """
+    T, D, V, dt = _head_common(h, W)
+    N = 0
+    if ids is not None:
+        _need(ids, "ids", torch.int32)
+        if ids.dim() not in (1, 2) or ids.shape[0] != T:
+            raise ValueError("ids must be [T] or [T, N]")
+        N = 1 if ids.dim() == 1 else ids.shape[1]
+    with torch.cuda.device(h.device):
+        nbytes, _ = token_logprobs_workspace(T, D, V, N, top_k, h.dtype)
+        if ids is not None and logp is None:
+            logp = torch.empty(ids.shape, dtype=torch.float32, device=h.device)
+        if ids is None and logp is not None:
+            raise ValueError("logp was given without ids")
+        if stats is None:
+            stats = torch.empty((2, T), dtype=torch.float32, device=h.device)
+        if top_k == 0 and (top_ids is not None or top_logp is not None):
+            raise ValueError("top_ids or top_logp was given without top_k")
+        if top_k and top_ids is None:
+            top_ids = torch.empty((T, top_k), dtype=torch.int32, device=h.device)
+        if top_k and top_logp is None:
+            top_logp = torch.empty((T, top_k), dtype=torch.float32, device=h.device)
+        _head_rows(logp, "logp", torch.float32, ids.shape if ids is not None else ())
+        _head_rows(stats, "stats", torch.float32, (2, T))
+        _head_rows(top_ids, "top_ids", torch.int32, (T, top_k))
+        _head_rows(top_logp, "top_logp", torch.float32, (T, top_k))
+        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
+        _same_device(h, ids=ids, logp=logp, stats=stats, top_ids=top_ids, top_logp=top_logp, status=status)
+        check("mls_token_logprobs",
+              lib().mls_token_logprobs(T, D, V, N, _ptr(ids), h.data_ptr(), W.data_ptr(), dt, _ptr(logp),
+                                       stats.data_ptr(), top_k, _ptr(top_ids), _ptr(top_logp), workspace.data_ptr(),
+                                       ws_bytes, _ptr(status), _stream_ptr(stream)))
+    return logp, stats, top_ids, top_logp
+
+
+def token_logprobs_bwd_workspace(T: int, D: int, V: int, N: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """(bytes, smallest accepted bytes) of token_logprobs_bwd (see mls_token_logprobs_bwd_workspace)."""
+    n, least = ctypes.c_size_t(), ctypes.c_size_t()
+    check("mls_token_logprobs_bwd_workspace",
+          lib().mls_token_logprobs_bwd_workspace(T, D, V, N, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
+                                                 ctypes.byref(n), ctypes.byref(least)))
+    return n.value, least.value
+
+
+def token_logprobs_bwd(ids: torch.Tensor, h: torch.Tensor, W: torch.Tensor, stats: torch.Tensor,
+                       g_logp: torch.Tensor, g_entropy: Optional[torch.Tensor] = None, *, dh=None, dW=None,
+                       dW_dtype: torch.dtype = torch.float32, accumulate_dW: bool = False, want_dh: bool = True,
+                       want_dW: bool = True, workspace=None, status=None, stream=None):
+    """Gradients of token_logprobs' log probabilities (g_logp, the shape of ids) and entropies (g_entropy [T])
+    with respect to h and W (see mls_token_logprobs_bwd).  Returns (dh or None, dW or None); dW is fp32, or
+    bf16 with dW_dtype=torch.bfloat16."""
+    T, D, V, dt = _head_common(h, W)
+    _need(ids, "ids", torch.int32)
+    if ids.dim() not in (1, 2) or ids.shape[0] != T:
+        raise ValueError("ids must be [T] or [T, N]")
+    N = 1 if ids.dim() == 1 else ids.shape[1]
+    with torch.cuda.device(h.device):
+        nbytes, _ = token_logprobs_bwd_workspace(T, D, V, N, h.dtype)
+        _head_rows(stats, "stats", torch.float32, (2, T))
+        _head_rows(g_logp, "g_logp", torch.float32, ids.shape)
+        _head_rows(g_entropy, "g_entropy", torch.float32, (T,))
+        dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
+        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
+        _same_device(h, ids=ids, stats=stats, g_logp=g_logp, g_entropy=g_entropy, status=status)
+        check("mls_token_logprobs_bwd",
+              lib().mls_token_logprobs_bwd(T, D, V, N, ids.data_ptr(), h.data_ptr(), W.data_ptr(), dt,
+                                           stats.data_ptr(), g_logp.data_ptr(), _ptr(g_entropy), _ptr(dh), _ptr(dW),
+                                           dW_code, int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes,
+                                           _ptr(status), _stream_ptr(stream)))
+    return dh, dW
+
+
+def topk_distill_workspace(T: int, D: int, V: int, K: int, dtype: torch.dtype) -> Tuple[int, int, int, int]:
+    """(forward bytes, smallest, backward bytes, smallest) of the distillation (see mls_topk_distill_workspace)."""
+    v = [ctypes.c_size_t() for _ in range(4)]
+    check("mls_topk_distill_workspace",
+          lib().mls_topk_distill_workspace(T, D, V, K, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
+                                           *[ctypes.byref(x) for x in v]))
+    return tuple(x.value for x in v)
+
+
+def _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W):
+    T, D, V, dt = _head_common(h, W)
+    _need(teacher_ids, "teacher_ids", torch.int32, 2)
+    K = teacher_ids.shape[1]
+    _head_rows(y, "y", torch.int32, (T,))
+    _head_rows(teacher_ids, "teacher_ids", torch.int32, (T, K))
+    _head_rows(teacher_logits, "teacher_logits", torch.float32, (T, K))
+    _head_rows(token_weights, "token_weights", torch.float32, (T,))
+    _same_device(h, y=y, teacher_ids=teacher_ids, teacher_logits=teacher_logits, token_weights=token_weights)
+    return T, D, V, K, dt
+
+
+def topk_distill_fwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, h: torch.Tensor,
+                     W: torch.Tensor, alpha_d: float = 0.3, *, token_weights: Optional[torch.Tensor] = None,
+                     losses=None, stats=None, workspace=None, status=None, stream=None):
+    """Next-token cross-entropy mixed with the cross-entropy to a teacher's top logits (teacher_ids int32 [T, K],
+    -1 where absent; teacher_logits f32 [T, K]; see mls_topk_distill_fwd).
+
+    Returns (losses [3] = mean cross-entropy, mean distillation term, their mix; stats [3, T] = log-sum-exp and
+    the two terms of every token)."""
+    T, D, V, K, dt = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W)
+    with torch.cuda.device(h.device):
+        nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[0]
+        if losses is None:
+            losses = torch.empty(3, dtype=torch.float32, device=h.device)
+        if stats is None:
+            stats = torch.empty((3, T), dtype=torch.float32, device=h.device)
+        _head_rows(losses, "losses", torch.float32, (3,))
+        _head_rows(stats, "stats", torch.float32, (3, T))
+        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
+        _same_device(h, losses=losses, stats=stats, status=status)
+        check("mls_topk_distill_fwd",
+              lib().mls_topk_distill_fwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+                                         _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
+                                         losses.data_ptr(), stats.data_ptr(), workspace.data_ptr(), ws_bytes,
+                                         _ptr(status), _stream_ptr(stream)))
+    return losses, stats
+
+
+def topk_distill_bwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, h: torch.Tensor,
+                     W: torch.Tensor, stats: torch.Tensor, alpha_d: float = 0.3, grad_scale: float = 1.0, *,
+                     token_weights: Optional[torch.Tensor] = None, dh=None, dW=None,
+                     dW_dtype: torch.dtype = torch.float32, accumulate_dW: bool = False, want_dh: bool = True,
+                     want_dW: bool = True, workspace=None, status=None, stream=None):
+    """Gradients of topk_distill_fwd's mixed loss times grad_scale with respect to h and W (see
+    mls_topk_distill_bwd).  Returns (dh or None, dW or None)."""
+    T, D, V, K, dt = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W)
+    with torch.cuda.device(h.device):
+        nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[2]
+        _head_rows(stats, "stats", torch.float32, (3, T))
+        dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
+        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
+        _same_device(h, stats=stats, status=status)
+        check("mls_topk_distill_bwd",
+              lib().mls_topk_distill_bwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+                                         _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
+                                         stats.data_ptr(), float(grad_scale), _ptr(dh), _ptr(dW), dW_code,
+                                         int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes, _ptr(status),
+                                         _stream_ptr(stream)))
+    return dh, dW
+
+
 def status_read(status: torch.Tensor, stream=None) -> Tuple[int, int]:
     """Synchronises, returns (status code, raw flag word) and clears the word."""
     out = ctypes.c_int32()

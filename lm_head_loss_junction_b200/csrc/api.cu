@@ -132,6 +132,8 @@ mls_status apply_options(const mls_loss_options* opts, LossProblem* p) {
 
 namespace mls {
 
+mls_status check_device() { return device_ok(); }
+
 mls_status check_junction_bwd_args(const int32_t* x, int64_t T, const void* o_m, int64_t D_m, const void* e_next,
                                    int64_t V, int64_t delta, const void* dy, const void* do_m, const void* de_rows,
                                    const float* dE_table, uint32_t variant, mls_dtype dt) {

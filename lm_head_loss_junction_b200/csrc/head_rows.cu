@@ -1,0 +1,567 @@
+// Per-token kernels of the single-exit LM-head operators: the entry lists, the
+// merge of the partial statistics, and the top alternatives.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "head.h"
+
+namespace mls {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------ entry lists
+// One warp per token turns the token's ids into a list sorted by id (ties by
+// position), with the position (forward) or the coefficient over the row scale
+// (backward); then the first entry of every split, one lane per token so that
+// the bytes of 32 tokens are written together.  A few microseconds: the table
+// of one byte per token and split is what it writes most.
+constexpr int kEntryTokens = 32;
+constexpr int kMaxTot = kMaxEntries + 1;
+constexpr int kPerLane = (kMaxTot + 31) / 32;
+
+struct EntrySmem {
+  int id[kEntryTokens][kMaxTot];
+  int sorted[kEntryTokens][kMaxTot];
+  int count[kEntryTokens];
+};
+
+__device__ __forceinline__ float pow2_of(float m) {
+  if (!(m > 0.f) || !(m <= 3.4e38f)) return m == 0.f ? 0.f : 1.f;
+  int e = ilogbf(m);
+  e = e < -126 ? -126 : (e > 126 ? 126 : e);
+  return ldexpf(1.f, e);
+}
+
+__global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn in, const HeadEntries out,
+                                                           bool backward, int n_splits, int32_t* status) {
+  __shared__ EntrySmem s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kEntryTokens;
+  const int N = in.N, tot = out.Ntot;
+  for (int i = warp; i < kEntryTokens; i += 8) {
+    const int64_t t = t0 + i;
+    if (t >= in.T) break;
+    int id[kPerLane];
+    float c[kPerLane];
+    bool there[kPerLane];
+    bool bad = false;
+    const float w = in.weights != nullptr ? in.weights[t] : 1.f;
+    const int32_t y = in.y != nullptr ? in.y[t] : 0;
+    // a token with a bad target is left out; one of weight 0 has no gradient, but terms of its own in stats
+    const bool out_y = in.y != nullptr && (y < 0 || y >= in.V);
+    const bool skip = out_y || (backward && w == 0.f);
+    if (out_y && w != 0.f) bad = true;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int j = k * 32 + lane;
+      id[k] = -1;
+      c[k] = 0.f;
+      if (j < N) {
+        id[k] = in.ids[t * N + j];
+        if (id[k] != -1 && (id[k] < 0 || id[k] >= in.V)) bad = true;
+      } else if (j == N && in.y != nullptr) {
+        id[k] = y;
+      }
+      there[k] = !skip && j < tot && id[k] >= 0 && id[k] < in.V;
+    }
+    float A = 0.f, B = 0.f, scale = 0.f;
+    if (backward) {
+      float most = 0.f;
+      if (in.y == nullptr) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          if (there[k]) c[k] = in.g_logp[t * N + k * 32 + lane];
+          sum += c[k];
+          most = fmaxf(most, fabsf(c[k]));
+        }
+        sum = warp_sum(sum);
+        B = in.g_entropy != nullptr ? -in.g_entropy[t] : 0.f;
+        A = -sum + (in.g_entropy != nullptr ? B * in.stats[in.T + t] : 0.f);
+        most = fmaxf(warp_max(most), fmaxf(fabsf(sum), fabsf(B)));
+      } else {
+        float z[kPerLane], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const int j = k * 32 + lane;
+          z[k] = there[k] && j < N ? in.teacher[t * N + j] : -INFINITY;
+          top = fmaxf(top, z[k]);
+        }
+        top = warp_max(top);
+        const bool some = top > -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          z[k] = some && there[k] && k * 32 + lane < N ? expf(z[k] - top) : 0.f;
+          sum += z[k];
+        }
+        sum = warp_sum(sum);
+        const float wg = skip ? 0.f : w * in.grad;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const int j = k * 32 + lane;
+          if (there[k]) c[k] = j == N ? -wg * (1.f - in.alpha) : (some ? -wg * in.alpha * (z[k] / sum) : 0.f);
+          most = fmaxf(most, fabsf(c[k]));
+        }
+        A = wg * ((1.f - in.alpha) + (some ? in.alpha : 0.f));
+        most = fmaxf(warp_max(most), fabsf(A));
+      }
+      scale = pow2_of(most);
+      if (lane == 0) {
+        const float r = scale != 0.f ? 1.f / scale : 0.f;
+        out.row[t] = make_float4(in.stats[t], A * r, B * r, scale);
+        if (scale > 0.f) atomicMax(out.smax, __float_as_uint(scale));
+      }
+    }
+    if (__any_sync(kFull, bad) && lane == 0) set_flag(status, MLS_DEVFLAG_BAD_ID);
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int j = k * 32 + lane;
+      n += __popc(__ballot_sync(kFull, there[k]));
+      if (j < tot) s.id[i][j] = there[k] ? id[k] : INT32_MAX;
+    }
+    if (lane == 0) s.count[i] = n;
+    __syncwarp();
+    const float r = scale != 0.f ? 1.f / scale : 0.f;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int j = k * 32 + lane;
+      if (!there[k]) continue;
+      int rank = 0;
+      for (int o = 0; o < tot; ++o) {
+        const int other = s.id[i][o];
+        rank += other < id[k] || (other == id[k] && o < j);
+      }
+      s.sorted[i][rank] = id[k];
+      out.e[t * tot + rank] = make_int2(id[k], backward ? __float_as_int(c[k] * r) : j);
+    }
+  }
+  __syncthreads();
+  const int64_t t = t0 + lane;
+  if (t < in.T) {
+    const int n = s.count[lane];
+    for (int sp = warp; sp <= n_splits; sp += 8) {
+      const int64_t edge = static_cast<int64_t>(sp) * kHeadSplit;
+      int lo = 0, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s.sorted[lane][mid] < edge) lo = mid + 1; else hi = mid;
+      }
+      out.first[static_cast<int64_t>(sp) * in.T + t] = static_cast<uint8_t>(lo);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge of partial statistics
+// (m, z, u) of two column sets -> of their union.
+__device__ __forceinline__ void merge_part(float& m, float& z, float& u, float m2, float z2, float u2) {
+  const float top = fmaxf(m, m2);
+  if (!(top > -INFINITY)) return;                        // nothing on either side (or NaN below)
+  if (z > 0.f || z != z) {
+    const float d = m - top, f = exp2f(d * kLog2e);
+    u = f * fmaf(d, z, u);
+    z *= f;
+  }
+  if (z2 > 0.f || z2 != z2) {
+    const float d = m2 - top, f = exp2f(d * kLog2e);
+    u = fmaf(f, fmaf(d, z2, u2), u);
+    z = fmaf(f, z2, z);
+  }
+  m = top;
+}
+
+__device__ __forceinline__ void warp_merge(float& m, float& z, float& u) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(kFull, m, o), z2 = __shfl_xor_sync(kFull, z, o), u2 = __shfl_xor_sync(kFull, u, o);
+    // the lower lane's part first on both sides, so that all lanes hold the same bits
+    if (threadIdx.x & o) {
+      float a = m2, b = z2, c = u2;
+      merge_part(a, b, c, m, z, u);
+      m = a;
+      z = b;
+      u = c;
+    } else {
+      merge_part(m, z, u, m2, z2, u2);
+    }
+  }
+}
+
+__device__ __forceinline__ float entry_logit(const HeadFinish& f, int64_t t, int tot, int j, int id) {
+  return f.picked != nullptr ? f.picked[t * tot + j] : f.logits[t * f.ld + id];
+}
+
+// The token's outputs that need only the statistics, by one warp.  A log
+// probability is (l - m) - log z: both are small where it is, lse is not.
+// fine: logits of the given tokens in 64 bits, or NULL.
+__device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int lane, float m, float logz, float mean,
+                                             const double* fine) {
+  if (lane == 0) f.stats[t] = m + logz;
+  bool bad = false;
+  if (f.y == nullptr) {
+    if (lane == 0) f.stats[f.ldT + t] = logz - mean;
+    for (int j = lane; j < f.N; j += 32) {
+      const int id = f.ids[t * f.N + j];
+      const bool there = id >= 0 && id < f.V;
+      float d = 0.f;
+      if (there) d = fine != nullptr ? static_cast<float>(fine[j] - m) : entry_logit(f, t, f.N, j, id) - m;
+      f.logp[t * f.N + j] = there ? d - logz : 0.f;
+      bad |= !there && id != -1;
+    }
+  } else {
+    const int tot = f.N + 1;
+    const float w = f.weights != nullptr ? f.weights[t] : 1.f;
+    const int y = f.y[t];
+    const bool out = y < 0 || y >= f.V;      // its logits were not picked
+    bad = out && w != 0.f;
+    float top = -INFINITY;
+    for (int j = lane; j < f.N; j += 32) {
+      const int id = f.ids[t * f.N + j];
+      const bool there = id >= 0 && id < f.V;
+      if (there) top = fmaxf(top, f.teacher[t * f.N + j]);
+      bad |= !there && id != -1;
+    }
+    top = warp_max(top);
+    const bool some = top > -INFINITY;
+    float sum = 0.f, kd = 0.f;
+    if (some && !out)
+      for (int j = lane; j < f.N; j += 32) {
+        const int id = f.ids[t * f.N + j];
+        if (id < 0 || id >= f.V) continue;
+        const float p = expf(f.teacher[t * f.N + j] - top);
+        sum += p;
+        if (p != 0.f) kd = fmaf(p, logz - (entry_logit(f, t, tot, j, id) - m), kd);
+      }
+    sum = warp_sum(sum);
+    kd = warp_sum(kd);
+    kd = some && !out ? kd / sum : 0.f;
+    if (lane == 0) {
+      const float ce = out ? 0.f : logz - (entry_logit(f, t, tot, f.N, y) - m);
+      f.stats[f.ldT + t] = ce;
+      f.stats[2 * f.ldT + t] = kd;
+      const bool counts = !out && w != 0.f;  // 0 times a term that is not a number is not 0
+      const float wce = counts ? w * ce : 0.f, wkd = counts ? w * kd : 0.f;
+      f.terms[t] = wce;
+      f.terms[f.ldT + t] = wkd;
+      f.terms[2 * f.ldT + t] = fmaf(f.alpha, wkd, (1.f - f.alpha) * wce);
+    }
+  }
+  if (__any_sync(kFull, bad) && lane == 0) set_flag(f.status, MLS_DEVFLAG_BAD_ID);
+}
+
+__global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= f.T) return;
+  float m = -INFINITY, z = 0.f, u = 0.f;
+  for (int s = lane; s < f.n_splits; s += 32) {
+    const HeadPart p = __ldg(f.part + t * f.n_splits + s);
+    merge_part(m, z, u, p.x, p.y, p.z);
+  }
+  warp_merge(m, z, u);
+  finish_token(f, t, lane, m, logf(z), u / z, nullptr);
+}
+
+// ------------------------------------------------------------------ top alternatives
+// One block per token.  The C = min(V, K + 8) largest logits by (value
+// descending, id ascending) lie in the C splits with the largest maxima by
+// (maximum descending, split ascending): were one of them in another split,
+// each chosen split's first maximum would come before it.  So only those
+// splits' logits are read, those below the C-th largest maximum are dropped,
+// and the C-th key among the rest is found by radix selection.  The candidates
+// are then ranked by products in 64 bits (exact enough that only equal logits
+// tie), so the ids do not depend on the tile a token fell into.
+// The tensor cores' accumulation truncates, which shrinks a logit by about
+// D 1e-9 of itself (2e-6 at D = 2304); the candidates' terms of z and u, the
+// ones that weigh, are replaced by those of the 64-bit logits, and so are the
+// given tokens' logits.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  f += 0.f;                                              // -0 ranks as 0
+  const uint32_t u = __float_as_uint(f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+__device__ __forceinline__ uint64_t top_key(float v, uint32_t index) {
+  return static_cast<uint64_t>(ordered(v)) << 32 | ~index;
+}
+
+constexpr int kTopThreads = 256;
+
+// The k-th largest of n distinct keys (1 <= k <= n) as a lower bound: exactly k
+// keys are at or above the returned value.  All threads of the block call it.
+__device__ uint64_t select_kth(const uint64_t* keys, int n, int k, int* hist, int* chosen) {
+  uint64_t prefix = 0;
+  int shift = 56;
+  for (; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kTopThreads) hist[i] = 0;
+    __syncthreads();
+    const uint64_t above = shift == 56 ? 0 : ~uint64_t(0) << (shift + 8);
+    for (int i = threadIdx.x; i < n; i += kTopThreads) {
+      const uint64_t key = keys[i];
+      if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // bins from the top, eight per lane: which bin holds the k-th, and how many lie above it
+      const int lane = threadIdx.x;
+      int own[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        own[i] = hist[255 - (lane * 8 + i)];
+        sum += own[i];
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, before, o);
+        if (lane >= o) before += v;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < k && k <= before + own[i]) {
+          chosen[0] = 255 - (lane * 8 + i);
+          chosen[1] = k - before;
+          chosen[2] = own[i];
+        }
+        before += own[i];
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint64_t>(chosen[0]) << shift;
+    k = chosen[1];
+    const bool whole = chosen[2] == k;
+    __syncthreads();
+    if (whole) break;                                    // the whole bin is taken
+  }
+  return prefix;
+}
+
+template <bool BF16>
+__device__ __forceinline__ double dot64(const void* h, const void* w, int64_t D, int lane) {
+  double acc = 0.0;
+  if (BF16) {
+    // a product of two bf16 values is exact in fp32
+    const uint4* a = static_cast<const uint4*>(h);
+    const uint4* b = static_cast<const uint4*>(w);
+    for (int64_t i = lane; i < D / 8; i += 32) {
+      float x[8], y[8];
+      bf16x8_to_f32(__ldg(a + i), x);
+      bf16x8_to_f32(__ldg(b + i), y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc += static_cast<double>(x[k] * y[k]);
+    }
+  } else {
+    const float* a = static_cast<const float*>(h);
+    const float* b = static_cast<const float*>(w);
+    for (int64_t i = lane; i < D; i += 32) acc = fma(static_cast<double>(a[i]), static_cast<double>(b[i]), acc);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+  return acc;
+}
+
+struct TopSmem {
+  int hist[256];
+  int chosen[4];
+  float part[kTopThreads / 32][3];
+  int count;
+  int n_sel;
+  int sel[kMaxEntries + kTopMore];
+  uint64_t fin[kMaxEntries + kTopMore];
+  double fine[kMaxEntries + kTopMore];
+  double given[kMaxEntries];
+  float dz[kMaxEntries + kTopMore], du[kMaxEntries + kTopMore];   // by rank: a fixed order of summation
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C) {
+  extern __shared__ uint8_t raw[];
+  TopSmem& s = *reinterpret_cast<TopSmem*>(raw);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x;
+  const int n_splits = f.n_splits;
+
+  // the statistics, and the splits' maxima as keys
+  float m = -INFINITY, z = 0.f, u = 0.f;
+  for (int i = threadIdx.x; i < n_splits; i += kTopThreads) {
+    const HeadPart p = __ldg(f.part + t * n_splits + i);
+    keys[i] = top_key(p.x, static_cast<uint32_t>(i));
+    merge_part(m, z, u, p.x, p.y, p.z);
+  }
+  warp_merge(m, z, u);
+  if (lane == 0) {
+    s.part[warp][0] = m;
+    s.part[warp][1] = z;
+    s.part[warp][2] = u;
+  }
+  if (threadIdx.x == 0) s.count = s.n_sel = 0;
+  __syncthreads();
+  m = -INFINITY, z = 0.f, u = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTopThreads / 32; ++i) merge_part(m, z, u, s.part[i][0], s.part[i][1], s.part[i][2]);
+
+  // the splits that hold the candidates, and a lower bound on the C-th largest logit
+  const int n_take = n_splits < C ? n_splits : C;
+  uint64_t bound = 0;
+  if (n_splits > C) bound = select_kth(keys, n_splits, C, s.hist, s.chosen);
+  uint32_t least = 0xffffffffu;
+  for (int i = threadIdx.x; i < n_splits; i += kTopThreads)
+    if (keys[i] >= bound) {
+      s.sel[atomicAdd(&s.n_sel, 1)] = i;
+      least = min(least, static_cast<uint32_t>(keys[i] >> 32));
+    }
+  least = __reduce_min_sync(kFull, least);
+  if (lane == 0) s.hist[warp] = static_cast<int>(least);
+  __syncthreads();
+  if (n_splits > C) {
+    for (int i = 0; i < kTopThreads / 32; ++i) least = min(least, static_cast<uint32_t>(s.hist[i]));
+  } else {
+    least = 0;
+  }
+  // their logits at or above it (keys is read no more: the list takes its place)
+  const float* row = f.logits + t * f.ld;
+  for (int i = warp; i < n_take; i += kTopThreads / 32) {
+    const int c0 = s.sel[i] * kHeadSplit;
+#pragma unroll
+    for (int k = 0; k < kHeadSplit / 32; ++k) {
+      const int col = c0 + k * 32 + lane;
+      if (col >= f.V) continue;
+      const uint64_t key = top_key(__ldg(row + col), static_cast<uint32_t>(col));
+      if (static_cast<uint32_t>(key >> 32) >= least) keys[atomicAdd(&s.count, 1)] = key;
+    }
+  }
+  __syncthreads();
+  const int n = s.count;
+  uint64_t last = 0;
+  if (n > C) last = select_kth(keys, n, C, s.hist, s.chosen);
+  if (threadIdx.x == 0) s.n_sel = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kTopThreads)
+    if (keys[i] >= last) s.fin[atomicAdd(&s.n_sel, 1)] = keys[i];
+  __syncthreads();
+
+  // ranked by their products in 64 bits (fewer than C only where logits are not numbers)
+  const int have = s.n_sel < C ? s.n_sel : C;
+  const size_t esize = BF16 ? 2 : 4;
+  const char* hrow = static_cast<const char*>(f.h) + t * f.D * esize;
+  for (int i = warp; i < have; i += kTopThreads / 32) {
+    const int64_t id = static_cast<int64_t>(~static_cast<uint32_t>(s.fin[i]));
+    const double v = dot64<BF16>(hrow, static_cast<const char*>(f.W) + id * f.D * esize, f.D, lane);
+    if (lane == 0) s.fine[i] = v;
+  }
+  for (int j = warp; j < f.N; j += kTopThreads / 32) {
+    const int id = f.ids[t * f.N + j];
+    if (id < 0 || id >= f.V) continue;
+    const double v = dot64<BF16>(hrow, static_cast<const char*>(f.W) + static_cast<int64_t>(id) * f.D * esize, f.D, lane);
+    if (lane == 0) s.given[j] = v;
+  }
+  __syncthreads();
+  int rank = kMaxEntries + kTopMore;
+  uint32_t id = 0;
+  if (threadIdx.x < have) {
+    id = ~static_cast<uint32_t>(s.fin[threadIdx.x]);
+    // doubles as ordered integers, so that every value (a NaN too) has one rank
+    auto order = [](double d) {
+      const int64_t b = __double_as_longlong(d + 0.0);
+      return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
+    };
+    const uint64_t mine = order(s.fine[threadIdx.x]);
+    rank = 0;
+    for (int i = 0; i < have; ++i) {
+      const uint64_t other = order(s.fine[i]);
+      rank += other > mine || (other == mine && ~static_cast<uint32_t>(s.fin[i]) < id);
+    }
+    const float was = unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)) - m;
+    const float is = static_cast<float>(s.fine[threadIdx.x] - m);
+    const float e0 = exp2f(was * kLog2e), e1 = exp2f(is * kLog2e);
+    s.dz[rank] = e1 - e0;
+    s.du[rank] = is * e1 - was * e0;
+  }
+  __syncthreads();
+  float dz = 0.f, du = 0.f;
+  for (int i = lane; i < have; i += 32) {
+    dz += s.dz[i];
+    du += s.du[i];
+  }
+  dz = warp_sum(dz);
+  du = warp_sum(du);
+  z += dz;
+  const float logz = logf(z);
+  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.given);
+  if (rank < f.K) {
+    f.top_ids[t * f.K + rank] = static_cast<int32_t>(id);
+    f.top_logp[t * f.K + rank] = static_cast<float>(s.fine[threadIdx.x] - m) - logz;
+  }
+  if (threadIdx.x >= have && threadIdx.x < f.K) {
+    f.top_ids[t * f.K + threadIdx.x] = -1;
+    f.top_logp[t * f.K + threadIdx.x] = NAN;
+  }
+}
+
+}  // namespace
+
+size_t head_entries_bytes(int64_t T, int64_t V, int Ntot, bool backward) {
+  size_t b = head_align(static_cast<size_t>(T) * Ntot * sizeof(int2));
+  b += head_align(static_cast<size_t>(head_splits(V) + 1) * T);
+  if (backward) b += head_align(static_cast<size_t>(T) * sizeof(float4)) + 256;
+  return b;
+}
+
+HeadEntries head_entries_layout(int64_t T, int64_t V, int Ntot, bool backward, void* ws) {
+  char* q = static_cast<char*>(ws);
+  HeadEntries e{};
+  e.Ntot = Ntot;
+  e.e = reinterpret_cast<int2*>(q);
+  q += head_align(static_cast<size_t>(T) * Ntot * sizeof(int2));
+  e.first = reinterpret_cast<uint8_t*>(q);
+  q += head_align(static_cast<size_t>(head_splits(V) + 1) * T);
+  if (backward) {
+    e.row = reinterpret_cast<float4*>(q);
+    q += head_align(static_cast<size_t>(T) * sizeof(float4));
+    e.smax = reinterpret_cast<unsigned int*>(q);
+  }
+  return e;
+}
+
+cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bool backward, int32_t* status,
+                             cudaStream_t st) {
+  if (backward) {
+    const cudaError_t err = cudaMemsetAsync(out.smax, 0, sizeof(unsigned int), st);
+    if (err != cudaSuccess) return err;
+  }
+  const unsigned grid = static_cast<unsigned>((in.T + kEntryTokens - 1) / kEntryTokens);
+  head_entries_kernel<<<grid, 256, 0, st>>>(in, out, backward, static_cast<int>(head_splits(in.V)), status);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
+  head_finish_kernel<<<static_cast<unsigned>((f.T + 7) / 8), 256, 0, st>>>(f);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
+  const int C = static_cast<int>(f.V < f.K + kTopMore ? f.V : f.K + kTopMore);
+  const int take = f.n_splits < C ? f.n_splits : C;
+  const size_t list = static_cast<size_t>(take) * kHeadSplit;
+  const size_t n = list > static_cast<size_t>(f.n_splits) ? list : static_cast<size_t>(f.n_splits);
+  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + n * sizeof(uint64_t);
+  auto fn = f.bf16 ? head_top_kernel<true> : head_top_kernel<false>;
+  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  fn<<<static_cast<unsigned>(f.T), kTopThreads, smem, st>>>(f, C);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace mls

@@ -1,0 +1,803 @@
+// Tensor-core (tcgen05 + TMEM + TMA) kernels of the single-exit LM-head
+// operators, bf16.
+//
+// One persistent kernel on CTA pairs computes 256 x 256 output tiles
+// (tcgen05.mma.cta_group::2, each CTA holding 128 rows of A, half of B and its
+// half of the fp32 accumulator in TMEM, two accumulator buffers) and differs
+// in what the eight epilogue warps of each CTA do with the accumulator:
+//   stats   logits h W^T of 256 tokens x 256 columns -> per token and 128-column
+//           split (max, sum e, sum of (l - max) e), and the logits of the
+//           token's entries; the logits themselves are not written
+//   logits  the same statistics, and the logits in fp32 (for the alternatives)
+//   grad    the logits again -> G' = q (A + B (l - lse)) + entries in fp16
+//   dh      G' W (K = columns of the chunk), scaled per row
+//   dw      G'^T h (K = tokens)
+// All five are bound by the tensor pipe once T passes a few hundred tokens and
+// by reading W below that.
+//
+// G' is fp16 (11-bit significand), not bf16 (8): the few large entries of a
+// peaked row dominate the gradient's error.  A row is stored divided by a
+// power of two s_t near the row's largest coefficient, so that rows of very
+// different weight keep the same relative precision; dh multiplies by s_t in
+// the epilogue and dw reads h rows that were multiplied by s_t when they were
+// copied to fp16 (powers of two change no significand).
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <atomic>
+#include <mutex>
+
+#include "head.h"
+#include "umma.cuh"
+
+namespace mls {
+
+namespace {
+
+constexpr int kBM = 128;                 // rows of A per CTA
+constexpr int kBN = 256;                 // columns of a tile
+constexpr int kBK = 64;                  // one 128-byte swizzle row of 16-bit values
+constexpr int kUK = 16;                  // K per tcgen05.mma
+constexpr int kStages = 6;               // 32 KB per stage and CTA
+constexpr int kEpiWarps = 8;             // two per TMEM lane quadrant, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kStageRow = 80;            // bytes of a staged row of 32 fp16 (padded against bank conflicts)
+constexpr int kGroupM = 8;               // row tiles per raster group: they share their A panels in L2
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMasked = -3.0e38f;      // logit of a column past V: finite, so that 0 * it is 0
+
+enum Epi { kStats, kLogits, kGrad, kDh, kDw };
+
+struct TileMaps {
+  CUtensorMap a, b;
+};
+
+struct TileArgs {
+  int rows, cols;                  // extents of the output
+  int kblocks;
+  int n_mt, tiles;                 // 256-row tiles, all tiles
+  // stats, logits, grad
+  int v0;                          // vocabulary id of column 0
+  int n_splits;                    // splits of a row of part
+  HeadPart* part;
+  float* logits;
+  int64_t ld;                      // row stride of logits or G'
+  const int2* e;
+  const uint8_t* first;
+  int64_t ld_first;
+  int Ntot;
+  float* picked;
+  const float4* row;
+  __half* G;
+  int gcols;                       // columns of G' that are written (a multiple of 64)
+  // dh, dw
+  void* out;
+  float* acc;                      // dh partial sums of earlier chunks [rows][cols] (NULL: none)
+  int accumulate;
+  const float* inv;                // device: 1 / scale of the fp16 copy
+  const unsigned int* smax;        // device: largest row scale (dw)
+  int32_t* status;
+};
+
+struct __align__(1024) TileSmem {
+  uint8_t a[kStages][kBM * kBK * 2];
+  uint8_t b[kStages][(kBN / 2) * kBK * 2];
+  uint8_t stage[kEpiWarps][32 * kStageRow];
+  uint64_t full[kStages];          // leader: both CTAs' bytes
+  uint64_t empty[kStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];              // leader: 16 epilogue warps
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  const bool ok = mbar_wait(bar, parity, abort, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tile_at(const TileArgs& a, int n_nt, int i, int& mt, int& nt) {
+  const int per_group = kGroupM * n_nt;
+  const int g = i / per_group;
+  const int first = g * kGroupM;
+  const int gm = min(kGroupM, a.n_mt - first);
+  const int r = i - g * per_group;
+  nt = r / gm;
+  mt = first + r % gm;
+}
+
+__device__ __forceinline__ uint32_t pack_g2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Columns at or past `left` of a 32-column chunk do not exist.
+__device__ __forceinline__ void mask_columns(float (&r)[32], int left) {
+  if (left < 32) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k >= left) r[k] = kMasked;
+  }
+}
+
+// The entries of one token inside its split, in ascending id order.
+struct EntryWalk {
+  const int2* p;
+  int n;
+  int2 cur;
+  __device__ __forceinline__ void start(const TileArgs& a, bool valid, int t, int split) {
+    n = 0;
+    if (valid) {
+      const int b = a.first[static_cast<int64_t>(split) * a.ld_first + t];
+      n = a.first[static_cast<int64_t>(split + 1) * a.ld_first + t] - b;
+      p = a.e + static_cast<int64_t>(t) * a.Ntot + b;
+    }
+    next();
+  }
+  __device__ __forceinline__ void next() {
+    cur = make_int2(INT32_MAX, 0);
+    if (n > 0) {
+      cur = __ldg(p++);
+      --n;
+    }
+  }
+};
+
+// A_MN / B_MN: the operand is stored with its M / N dimension contiguous
+// (boxes of 64 x 64), otherwise with K contiguous.
+template <Epi EPI>
+struct Layout {
+  static constexpr bool a_mn = EPI == kDw;
+  static constexpr bool b_mn = EPI == kDh || EPI == kDw;
+  static constexpr bool f16 = EPI == kDh || EPI == kDw;
+};
+
+template <Epi EPI, bool OUT_BF16>
+__device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_t acc_col, int warp, int lane,
+                                         int64_t row, int col_tile, int half, uint64_t* tempty) {
+  const bool valid = row < a.rows;
+  const int c0 = col_tile + half * 128;
+  auto release = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+  };
+  if constexpr (EPI == kStats || EPI == kLogits) {
+    if (c0 >= a.cols) {
+      release();
+      return;
+    }
+    const int t = static_cast<int>(row);
+    const int split = c0 / kHeadSplit;
+    EntryWalk en;
+    if constexpr (EPI == kStats) en.start(a, valid, t, split);
+    float m = -INFINITY, z = 0.f, u = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float r[32];
+      tmem_ld32(acc_col + c * 32, r);
+      if (c == 3) release();
+      const int col = c0 + c * 32;
+      if (col >= a.cols) continue;
+      if constexpr (EPI == kStats) {
+        while (__any_sync(0xffffffffu, en.cur.x < col + 32)) {
+          const bool mine = en.cur.x < col + 32;
+          const int k0 = mine ? en.cur.x - col : -1;
+          float v = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v = k == k0 ? r[k] : v;
+          if (mine) {
+            a.picked[static_cast<int64_t>(t) * a.Ntot + en.cur.y] = v;
+            en.next();
+          }
+        }
+      }
+      mask_columns(r, a.cols - col);
+      if constexpr (EPI == kLogits) {
+        if (valid) {
+          float4* dst = reinterpret_cast<float4*>(a.logits + row * a.ld + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+      }
+      float cm = r[0];
+#pragma unroll
+      for (int k = 1; k < 32; ++k) cm = fmaxf(cm, r[k]);
+      if (cm > m) {
+        // move the sums to the new maximum: (l - m') e^(l - m') = f ((l - m) + (m - m')) e^(l - m)
+        if (z > 0.f) {
+          const float dm = m - cm;
+          const float f = exp2f(dm * kLog2e);
+          u = f * fmaf(dm, z, u);
+          z *= f;
+        }
+        m = cm;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float d = r[k] - m;
+        const float e = exp2f(d * kLog2e);
+        z += e;
+        u = fmaf(d, e, u);
+      }
+    }
+    if (valid) a.part[row * a.n_splits + split] = make_float4(m, z, u, 0.f);
+  } else if constexpr (EPI == kGrad) {
+    if (c0 >= a.gcols) {
+      release();
+      return;
+    }
+    const int t = static_cast<int>(row);
+    const float4 ri = valid ? __ldg(a.row + t) : make_float4(0.f, 0.f, 0.f, 0.f);   // (lse, A, B, s)
+    const bool live = valid && !(ri.w == 0.f);
+    EntryWalk en;
+    en.start(a, live && c0 < a.cols, t, (a.v0 + c0) / kHeadSplit);
+    uint8_t* stage = s.stage[warp - 2];
+    const int64_t row0 = row - lane;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float r[32];
+      tmem_ld32(acc_col + c * 32, r);
+      if (c == 3) release();
+      const int col = c0 + c * 32;
+      if (col >= a.gcols) continue;
+      const int left = a.cols - col;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float d = r[k] - ri.x;
+        const float g = exp2f(d * kLog2e) * fmaf(ri.z, d, ri.y);
+        r[k] = live && k < left ? g : 0.f;
+      }
+      while (__any_sync(0xffffffffu, en.cur.x - a.v0 < col + 32)) {
+        const bool mine = en.cur.x - a.v0 < col + 32;
+        const int k0 = mine ? en.cur.x - a.v0 - col : -1;
+        const float cf = __int_as_float(en.cur.y);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) r[k] += k == k0 ? cf : 0.f;
+        if (mine) en.next();
+      }
+      uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStageRow);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mine[k] = make_uint4(pack_g2(r[8 * k], r[8 * k + 1]), pack_g2(r[8 * k + 2], r[8 * k + 3]),
+                             pack_g2(r[8 * k + 4], r[8 * k + 5]), pack_g2(r[8 * k + 6], r[8 * k + 7]));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {        // 8 rows x 64 contiguous bytes per store instruction
+        const int piece = i * 32 + lane;
+        const int rr = piece >> 2, ch = piece & 3;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * kStageRow + ch * 16);
+        if (row0 + rr < a.rows) *reinterpret_cast<uint4*>(a.G + (row0 + rr) * a.ld + col + ch * 8) = v;
+      }
+      __syncwarp();
+    }
+  } else {
+    const float inv = __ldg(a.inv);
+    float alpha = inv;
+    if constexpr (EPI == kDw) alpha = inv * __uint_as_float(__ldg(a.smax));
+    const float rs = EPI == kDh && valid ? __ldg(&a.row[row].w) : 1.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float r[32];
+      tmem_ld32(acc_col + c * 32, r);
+      if (c == 3) release();
+      const int col = c0 + c * 32;
+      if (!valid || col >= a.cols) continue;
+      const int64_t off = row * a.cols + col;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) r[k] *= alpha;
+      if constexpr (OUT_BF16) {
+        if (EPI == kDh && a.acc != nullptr) {
+          const float4* ad = reinterpret_cast<const float4*>(a.acc + off);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 v = ad[k];
+            r[4 * k] += v.x;
+            r[4 * k + 1] += v.y;
+            r[4 * k + 2] += v.z;
+            r[4 * k + 3] += v.w;
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = r[8 * k + i] * rs;
+          dst[k] = f32_to_bf16x8(f);
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + off);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float4 v = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          if (a.accumulate) {
+            const float4 o = dst[k];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
+          dst[k] = v;
+        }
+      }
+    }
+  }
+}
+
+template <Epi EPI, bool OUT_BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    head_tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a) {
+  using L = Layout<EPI>;
+  extern __shared__ uint8_t smem_raw[];
+  TileSmem& s = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort = &s.abort;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int n_nt = a.tiles / a.n_mt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s.tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();        // every barrier of both CTAs exists before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int tile = pair; tile < a.tiles && ok; tile += npairs) {
+        int mt, nt;
+        tile_at(a, n_nt, tile, mt, nt);
+        const int row0 = mt * 2 * kBM + static_cast<int>(rank) * kBM;      // this CTA's rows of A
+        const int n0 = nt * kBN + static_cast<int>(rank) * (kBN / 2);      // and of B
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!mbar_wait(&s.empty[stage], phase ^ 1, abort, a.status)) { ok = false; break; }
+          const uint32_t lfull = mapa_shared(smem_u32(&s.full[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(&s.full[stage], 2 * (kBM + kBN / 2) * kBK * 2);
+          if (L::a_mn) {
+#pragma unroll
+            for (int j = 0; j < kBM / 64; ++j)
+              tma_load_2d_pair(&maps.a, lfull, s.a[stage] + j * (64 * kBK * 2), row0 + j * 64, kb * kBK);
+          } else {
+            tma_load_2d_pair(&maps.a, lfull, s.a[stage], kb * kBK, row0);
+          }
+          if (L::b_mn) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              tma_load_2d_pair(&maps.b, lfull, s.b[stage] + j * (64 * kBK * 2), n0 + j * 64, kb * kBK);
+          } else {
+            tma_load_2d_pair(&maps.b, lfull, s.b[stage], kb * kBK, n0);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok) {
+        // this CTA's loads complete on the leader's barrier: give them time to land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (leader CTA)
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = L::f16 ? idesc_f16(2 * kBM, kBN, L::a_mn, L::b_mn)
+                                        : idesc_bf16(2 * kBM, kBN, L::a_mn, L::b_mn);
+      // one tcgen05.mma further along K: 32 bytes inside the swizzled row, or 16 rows of 128 bytes
+      constexpr uint32_t a_step = L::a_mn ? (kUK * 128) >> 4 : (kUK * 2) >> 4;
+      constexpr uint32_t b_step = L::b_mn ? (kUK * 128) >> 4 : (kUK * 2) >> 4;
+      constexpr uint32_t a_lbo = L::a_mn ? 64 * kBK * 2 : 16;
+      constexpr uint32_t b_lbo = L::b_mn ? 64 * kBK * 2 : 16;
+      uint32_t stage = 0, phase = 0, iter = 0;
+      bool ok = true;
+      for (int tile = pair; tile < a.tiles && ok; tile += npairs, ++iter) {
+        const uint32_t buf = iter & 1;
+        if (!mbar_wait(&s.tempty[buf], ((iter >> 1) & 1) ^ 1, abort, a.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kBN;
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+          if (!mbar_wait(&s.full[stage], phase, abort, a.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = smem_desc_sw128(smem_u32(s.a[stage]), a_lbo, 1024);
+          const uint64_t db = smem_desc_sw128(smem_u32(s.b[stage]), b_lbo, 1024);
+#pragma unroll
+          for (int k = 0; k < kBK / kUK; ++k)
+            umma_bf16_pair(d, da + static_cast<uint64_t>(k * a_step), db + static_cast<uint64_t>(k * b_step), idesc,
+                           (kb | k) != 0);
+          const uint32_t e = smem_u32(&s.empty[stage]);
+          umma_commit_pair(mapa_shared(e, 0));
+          umma_commit_pair(mapa_shared(e, 1));
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+        if (ok) {
+          const uint32_t f = smem_u32(&s.tfull[buf]);
+          umma_commit_pair(mapa_shared(f, 0));
+          umma_commit_pair(mapa_shared(f, 1));
+        }
+      }
+      umma_commit_pair(mapa_shared(smem_u32(&s.drain), 0));
+      int dummy = 0;
+      (void)mbar_wait(&s.drain, 0, &dummy, a.status);     // every MMA done before TMEM is released
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;                               // TMEM lane quadrant this warp may read
+    const int half = (warp - 2) >> 2;
+    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    uint32_t iter = 0;
+    for (int tile = pair; tile < a.tiles; tile += npairs, ++iter) {
+      int mt, nt;
+      tile_at(a, n_nt, tile, mt, nt);
+      const uint32_t buf = iter & 1;
+      if (!warp_wait(&s.tfull[buf], (iter >> 1) & 1, abort, a.status)) break;
+      tc_fence_after();
+      const int64_t row = static_cast<int64_t>(mt) * 2 * kBM + rank * kBM + q * 32 + lane;
+      epilogue<EPI, OUT_BF16>(a, s, base + buf * kBN, warp, lane, row, nt * kBN, half, &s.tempty[buf]);
+    }
+  }
+
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync_all();        // no CTA leaves while its pair may still touch its memory
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ fp16 operand copies
+// dst[r][:] = fp16(src[r][:] * f_r), f_r = 1, or 64 times the row's scale over
+// the largest one (64: rows down to 2^-20 of the largest scale stay in fp16's
+// normal range at values near 1, values up to 512 do not pass it); tracks the largest magnitude.  kind::f16 takes A and B of one
+// type, so G' in fp16 needs W and h in fp16.  bf16's 8 significant bits fit in
+// fp16's 11: values in its normal range convert exactly.
+struct CopyArgs {
+  const uint4* src;
+  uint4* dst;
+  int64_t n_vec;
+  int vec_per_row;
+  const float4* row;               // row scales in .w (NULL: 1)
+  const unsigned int* smax;
+  unsigned int* maxbits;
+  float* inv;
+};
+
+__device__ __forceinline__ uint4 to_half8(const uint4& v, float f, float& mx) {
+  float x[8];
+  bf16x8_to_f32(v, x);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    // a row of scale 0 is left out, whatever it holds
+    const float lo = f == 0.f ? 0.f : x[2 * k] * f, hi = f == 0.f ? 0.f : x[2 * k + 1] * f;
+    mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
+    __half2 h = __floats2half2_rn(lo, hi);
+    w[k] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr float kRowLift = 64.f;
+
+__device__ __forceinline__ float copy_factor(const CopyArgs& a, int64_t i, float smax) {
+  if (a.row == nullptr) return 1.f;
+  return smax > 0.f ? a.row[i / a.vec_per_row].w / smax * kRowLift : 0.f;
+}
+
+__global__ void __launch_bounds__(256) head_copy_kernel(const CopyArgs a) {
+  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
+  float mx = 0.f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  for (; i + 3 * stride < a.n_vec; i += 4 * stride) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __ldg(a.src + i + k * stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
+  }
+  for (; i < a.n_vec; i += stride) a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax), mx);
+  mx = warp_max(mx);
+  if ((threadIdx.x & 31) == 0 && mx > 0.f) atomicMax(a.maxbits, __float_as_uint(mx));
+}
+
+// The copy again with a power-of-two scale when the largest magnitude is at or
+// past 2^15 or below 2^-10; the reciprocal of the scale for the epilogue.
+__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyArgs a) {
+  const float mx = __uint_as_float(*a.maxbits);
+  float s = 1.f;
+  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 1024.f))) {
+    int e = 13 - ilogbf(mx);
+    e = e < -126 ? -126 : (e > 126 ? 126 : e);
+    s = ldexpf(1.f, e);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
+  if (s == 1.f) return;
+  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
+  float unused = 0.f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.n_vec; i += stride)
+    a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax) * s, unused);
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// 2-D tensor of 16-bit elements [outer][ld], the first `inner` of each row
+// addressable (elements outside read as zero), 128-byte swizzled boxes.
+bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+              int box_outer, bool fp16) {
+  EncodeTiledFn enc = get_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int num_sms() {
+  int dev = 0, n = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+constexpr size_t kSmemBytes = sizeof(TileSmem) + 1024;
+
+// CTA pairs that can be resident at once: a persistent grid larger than that
+// would leave whole pairs waiting for a second wave.
+template <typename Kernel>
+int resident_pairs(Kernel fn) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    n = num_sms() / 2;
+  }
+  return n;
+}
+
+template <Epi EPI, bool OUT_BF16>
+cudaError_t run_tiles(const TileMaps& maps, TileArgs a, int64_t kdim, cudaStream_t st) {
+  const int64_t n_mt = (a.rows + 2 * kBM - 1) / (2 * kBM);
+  const int64_t wide = EPI == kGrad ? a.gcols : a.cols;
+  const int64_t tiles = n_mt * ((wide + kBN - 1) / kBN);
+  if (tiles > INT32_MAX - 1024) return cudaErrorInvalidValue;
+  a.n_mt = static_cast<int>(n_mt);
+  a.tiles = static_cast<int>(tiles);
+  a.kblocks = static_cast<int>((kdim + kBK - 1) / kBK);
+  auto fn = head_tile_kernel<EPI, OUT_BF16>;
+  cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+  if (err != cudaSuccess) return err;
+  const int resident = resident_pairs(fn);
+  const int pairs = a.tiles < resident ? a.tiles : resident;
+  fn<<<2 * pairs, kThreads, kSmemBytes, st>>>(maps, a);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t run_copy(const void* src, __half* dst, int64_t rows, int64_t D, const HeadEntries* scaled,
+                     unsigned int* maxbits, float* inv, cudaStream_t st) {
+  cudaError_t err = cudaMemsetAsync(maxbits, 0, sizeof(unsigned int), st);
+  if (err != cudaSuccess) return err;
+  CopyArgs a{};
+  a.src = static_cast<const uint4*>(src);
+  a.dst = reinterpret_cast<uint4*>(dst);
+  a.n_vec = rows * D / 8;
+  a.vec_per_row = static_cast<int>(D / 8);
+  if (scaled != nullptr) {
+    a.row = scaled->row;
+    a.smax = scaled->smax;
+  }
+  a.maxbits = maxbits;
+  a.inv = inv;
+  const int64_t want = (a.n_vec + 1023) / 1024, cap = 8 * static_cast<int64_t>(num_sms());
+  const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
+  head_copy_kernel<<<grid, 256, 0, st>>>(a);
+  head_rescale_kernel<<<grid, 256, 0, st>>>(a);
+  note_launches(2);
+  return cudaGetLastError();
+}
+
+// Backward workspace: [G' chunk: T x round_up(Vc, 64) f16][dh partial sums:
+// T x D f32, only with more than one chunk][h in fp16][the chunk's W rows in
+// fp16][copy scales].
+struct BwdWs {
+  int64_t ldg;
+  size_t g, acc, h16, w16, aux;
+  size_t total() const { return g + acc + h16 + w16 + aux; }
+};
+
+BwdWs bwd_layout(const HeadProblem& p, int64_t Vc) {
+  BwdWs w{};
+  w.ldg = (Vc + 63) / 64 * 64;
+  w.g = head_align(static_cast<size_t>(p.T) * w.ldg * 2);
+  w.acc = Vc < p.V ? head_align(static_cast<size_t>(p.T) * p.D * 4) : 0;
+  w.h16 = head_align(static_cast<size_t>(p.T) * p.D * 2);
+  w.w16 = head_align(static_cast<size_t>(Vc) * p.D * 2);
+  w.aux = 256;
+  return w;
+}
+
+}  // namespace
+
+cudaError_t head_tc_forward(const HeadProblem& p, const HeadForward& f, cudaStream_t st) {
+  TileMaps maps;
+  if (!make_map(&maps.a, f.h, p.D, f.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
+  if (!make_map(&maps.b, p.W, p.D, p.V, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
+  TileArgs a{};
+  a.rows = static_cast<int>(f.T);
+  a.cols = static_cast<int>(p.V);
+  a.n_splits = static_cast<int>(head_splits(p.V));
+  a.part = f.part;
+  a.logits = f.logits;
+  a.ld = f.ld;
+  a.e = f.en.e;
+  a.first = f.en.first;
+  a.ld_first = f.ld_first;
+  a.Ntot = f.en.Ntot;
+  a.picked = f.picked;
+  a.status = p.status;
+  return f.logits != nullptr ? run_tiles<kLogits, false>(maps, a, p.D, st) : run_tiles<kStats, false>(maps, a, p.D, st);
+}
+
+size_t head_tc_bwd_bytes(const HeadProblem& p, int64_t Vc) { return bwd_layout(p, Vc).total(); }
+
+// The widest chunk (the whole vocabulary, or equal chunks of a multiple of 256
+// columns) whose workspace fits; 0 when none does.
+int64_t head_tc_bwd_chunk(const HeadProblem& p, size_t budget) {
+  if (bwd_layout(p, p.V).total() <= budget) return p.V;
+  int64_t lo = 0, hi = (p.V - 1) / kBN;                 // chunks of kBN columns
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    if (bwd_layout(p, mid * kBN).total() <= budget) lo = mid; else hi = mid - 1;
+  }
+  if (lo == 0) return 0;
+  const int64_t n = (p.V + lo * kBN - 1) / (lo * kBN);
+  const int64_t even = ((p.V + n - 1) / n + kBN - 1) / kBN * kBN;
+  return even < lo * kBN ? even : lo * kBN;
+}
+
+cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* dh, void* dW, bool dW_bf16,
+                             int accumulate, void* ws, int64_t Vc, cudaStream_t st) {
+  const BwdWs w = bwd_layout(p, Vc);
+  char* q = static_cast<char*>(ws);
+  __half* G = reinterpret_cast<__half*>(q);
+  q += w.g;
+  float* acc = w.acc != 0 ? reinterpret_cast<float*>(q) : nullptr;
+  q += w.acc;
+  __half* h16 = reinterpret_cast<__half*>(q);
+  q += w.h16;
+  __half* w16 = reinterpret_cast<__half*>(q);
+  q += w.w16;
+  unsigned int* maxbits = reinterpret_cast<unsigned int*>(q);          // [0] W, [1] h
+  float* inv = reinterpret_cast<float*>(q + 64);
+  cudaError_t err = cudaSuccess;
+  if (dW != nullptr) {
+    err = run_copy(p.h, h16, p.T, p.D, &en, maxbits + 1, inv + 1, st);
+    if (err != cudaSuccess) return err;
+  }
+  for (int64_t v0 = 0; v0 < p.V; v0 += Vc) {
+    const int64_t n = v0 + Vc <= p.V ? Vc : p.V - v0;
+    const bool first = v0 == 0, last = v0 + n >= p.V;
+    const void* Wc = static_cast<const __nv_bfloat16*>(p.W) + v0 * p.D;
+    TileMaps maps;
+    TileArgs a{};
+    a.status = p.status;
+    // G' of the chunk
+    if (!make_map(&maps.a, p.h, p.D, p.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
+    if (!make_map(&maps.b, Wc, p.D, n, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
+    a.rows = static_cast<int>(p.T);
+    a.cols = static_cast<int>(n);
+    a.v0 = static_cast<int>(v0);
+    a.e = en.e;
+    a.first = en.first;
+    a.ld_first = p.T;
+    a.Ntot = en.Ntot;
+    a.row = en.row;
+    a.G = G;
+    a.ld = w.ldg;
+    a.gcols = static_cast<int>((n + 63) / 64 * 64);
+    err = run_tiles<kGrad, false>(maps, a, p.D, st);
+    if (err != cudaSuccess) return err;
+    if (dh != nullptr) {
+      err = run_copy(Wc, w16, n, p.D, nullptr, maxbits, inv, st);
+      if (err != cudaSuccess) return err;
+      TileArgs d{};
+      d.status = p.status;
+      d.rows = static_cast<int>(p.T);
+      d.cols = static_cast<int>(p.D);
+      d.inv = inv;
+      d.row = en.row;
+      if (!make_map(&maps.a, G, a.gcols, p.T, w.ldg, kBK, kBM, true)) return cudaErrorInvalidValue;
+      if (!make_map(&maps.b, w16, p.D, n, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (last) {
+        d.out = dh;
+        d.acc = first ? nullptr : acc;
+        err = run_tiles<kDh, true>(maps, d, n, st);
+      } else {
+        d.out = acc;
+        d.accumulate = first ? 0 : 1;
+        err = run_tiles<kDh, false>(maps, d, n, st);
+      }
+      if (err != cudaSuccess) return err;
+    }
+    if (dW != nullptr) {
+      TileArgs d{};
+      d.status = p.status;
+      d.rows = static_cast<int>(n);
+      d.cols = static_cast<int>(p.D);
+      d.inv = inv + 1;
+      d.smax = en.smax;
+      d.accumulate = accumulate;
+      if (!make_map(&maps.a, G, a.gcols, p.T, w.ldg, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (!make_map(&maps.b, h16, p.D, p.T, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (dW_bf16) {
+        d.out = static_cast<__nv_bfloat16*>(dW) + v0 * p.D;
+        err = run_tiles<kDw, true>(maps, d, p.T, st);
+      } else {
+        d.out = static_cast<float*>(dW) + v0 * p.D;
+        err = run_tiles<kDw, false>(maps, d, p.T, st);
+      }
+      if (err != cudaSuccess) return err;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace mls

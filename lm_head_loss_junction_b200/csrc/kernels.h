@@ -161,6 +161,9 @@ cudaError_t launch_loss_reduce(const float* terms, const LossProblem& p, float* 
 // Counts kernel launches issued by the library (diagnostics).
 void note_launches(int n);
 
+// MLS_OK when the current device is a compute-capability 10.0 GPU.
+mls_status check_device();
+
 // Set when the tensor-map encoder could not be obtained from the driver.
 bool tensor_map_encoder_available();
 
