@@ -495,8 +495,8 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  *              in 64 bits, so it does not depend on T, the workspace or the
  *              position.  -1 where fewer than K logits are numbers.
  *   top_logp   device f32 [T, K]: their log probabilities
- * Without alternatives MLS_BF16 never writes the logits; with them, the logits
- * of one block of tokens at a time go to the workspace in fp32.
+ * Without alternatives and past 128 tokens MLS_BF16 never writes the logits;
+ * otherwise those of one block of tokens at a time go to the workspace in fp32.
  */
 mls_status mls_token_logprobs_workspace(int64_t T, int64_t D, int64_t V, int N, int K, mls_dtype dt,
                                         size_t* bytes, size_t* min_bytes);

@@ -8,6 +8,7 @@ CUDA kernels; nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -321,112 +322,138 @@ def exit_agreement(h: List[torch.Tensor], W: List[torch.Tensor], stats: torch.Te
 
 
 # ---------------------------------------------------------------- single-exit LM-head operators
+# A decoding step's call is shorter on the GPU than a careless wrapper is on the host, so these check each
+# tensor with one expression, ask for the sizes of a shape once and take the raw stream.
+def _head_fit(t, name, dtype, shape, dev):
+    """Checks a tensor given by the caller: contiguous, of the dtype and shape, on the device of h."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    _need(t, name, dtype)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on the device of h")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
 def _head_common(h, W):
     _need(h, "h", ndim=2)
     _need(W, "W", h.dtype, 2)
-    if h.shape[1] != W.shape[1]:
+    (T, D), (V, DW) = h.shape, W.shape
+    if D != DW:
         raise ValueError("h must be [T, D] and W [V, D]")
     if W.device != h.device:
         raise ValueError("W must be on the device of h")
-    return h.shape[0], h.shape[1], W.shape[0], _dtype_code(h)
+    return T, D, V, _dtype_code(h), h.device
 
 
-def _same_device(h, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != h.device:
-            raise ValueError(f"{name} must be on the device of h")
+def _head_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream_ptr(stream)
 
 
-def _head_rows(t, name, dtype, shape):
-    """t as given, or None; checked to be contiguous, of the dtype and the shape."""
-    if t is None:
-        return None
-    _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+def _head_ids(ids, T, dev):
+    if ids.dim() not in (1, 2) or ids.shape[0] != T:
+        raise ValueError("ids must be [T] or [T, N]")
+    _head_fit(ids, "ids", torch.int32, ids.shape, dev)
+    return 1 if ids.dim() == 1 else ids.shape[1]
 
 
-def _head_workspace(ws, nbytes, h):
+def _head_workspace(ws, nbytes, dev):
     if ws is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=h.device), nbytes
-    _need(ws, "workspace")
-    _same_device(h, workspace=ws)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    _head_fit(ws, "workspace", ws.dtype, ws.shape, dev)
     return ws, ws.numel() * ws.element_size()
 
 
 def _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW):
     if not want_dh and dh is not None or not want_dW and dW is not None:
         raise ValueError("an output was given for a gradient that is not wanted")
-    if want_dh and dh is None:
+    if dh is not None:
+        _head_fit(dh, "dh", h.dtype, h.shape, h.device)
+    elif want_dh:
         dh = torch.empty_like(h)
-    if want_dW and dW is None:
+    if dW is not None:
+        _head_fit(dW, "dW", dW.dtype, W.shape, h.device)
+    elif want_dW:
         if accumulate_dW:
             raise ValueError("accumulate_dW needs dW")
         dW = torch.empty(W.shape, dtype=dW_dtype, device=W.device)
-    dh = _head_rows(dh, "dh", h.dtype, h.shape)
-    dW = _head_rows(dW, "dW", dW.dtype if dW is not None else None, W.shape)
-    _same_device(h, dh=dh, dW=dW)
     return dh, dW, _dtype_code(dW) if dW is not None else MLS_F32
 
 
+def _elsewhere(h):
+    """Whether h lives on another device than the current one (the library launches on the current one)."""
+    return h.is_cuda and h.device.index != torch.cuda.current_device()
+
+
+def _code_of(dtype):
+    return MLS_BF16 if dtype == torch.bfloat16 else MLS_F32
+
+
+@functools.lru_cache(maxsize=1024)
 def token_logprobs_workspace(T: int, D: int, V: int, N: int, top_k: int, dtype: torch.dtype) -> Tuple[int, int]:
     """(bytes, smallest accepted bytes) of token_logprobs (see mls_token_logprobs_workspace)."""
     n, least = ctypes.c_size_t(), ctypes.c_size_t()
     check("mls_token_logprobs_workspace",
-          lib().mls_token_logprobs_workspace(T, D, V, N, top_k, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
-                                             ctypes.byref(n), ctypes.byref(least)))
+          lib().mls_token_logprobs_workspace(T, D, V, N, top_k, _code_of(dtype), ctypes.byref(n),
+                                             ctypes.byref(least)))
     return n.value, least.value
 
 
 def token_logprobs(ids: Optional[torch.Tensor], h: torch.Tensor, W: torch.Tensor, *, top_k: int = 0, logp=None,
                    stats=None, top_ids=None, top_logp=None, workspace=None, status=None, stream=None):
     """Log probabilities of given tokens under softmax(h W^T), the entropy of that distribution and its top
-    alternatives, without writing the logits out (see mls_token_logprobs).
+    alternatives, without a T x V result (see mls_token_logprobs).
 
     ids: int32 [T] or [T, N] (-1: no token there), or None with top_k > 0.  Returns (logp of the shape of ids or
     None, stats [2, T] = log-sum-exp and entropy, top_ids [T, top_k] or None, top_logp [T, top_k] or None).
     """
-    T, D, V, dt = _head_common(h, W)
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return token_logprobs(ids, h, W, top_k=top_k, logp=logp, stats=stats, top_ids=top_ids, top_logp=top_logp,
+                                  workspace=workspace, status=status, stream=stream)
+    T, D, V, dt, dev = _head_common(h, W)
+    f32 = torch.float32
     N = 0
     if ids is not None:
-        _need(ids, "ids", torch.int32)
-        if ids.dim() not in (1, 2) or ids.shape[0] != T:
-            raise ValueError("ids must be [T] or [T, N]")
-        N = 1 if ids.dim() == 1 else ids.shape[1]
-    with torch.cuda.device(h.device):
-        nbytes, _ = token_logprobs_workspace(T, D, V, N, top_k, h.dtype)
-        if ids is not None and logp is None:
-            logp = torch.empty(ids.shape, dtype=torch.float32, device=h.device)
-        if ids is None and logp is not None:
-            raise ValueError("logp was given without ids")
-        if stats is None:
-            stats = torch.empty((2, T), dtype=torch.float32, device=h.device)
-        if top_k == 0 and (top_ids is not None or top_logp is not None):
-            raise ValueError("top_ids or top_logp was given without top_k")
-        if top_k and top_ids is None:
-            top_ids = torch.empty((T, top_k), dtype=torch.int32, device=h.device)
-        if top_k and top_logp is None:
-            top_logp = torch.empty((T, top_k), dtype=torch.float32, device=h.device)
-        _head_rows(logp, "logp", torch.float32, ids.shape if ids is not None else ())
-        _head_rows(stats, "stats", torch.float32, (2, T))
-        _head_rows(top_ids, "top_ids", torch.int32, (T, top_k))
-        _head_rows(top_logp, "top_logp", torch.float32, (T, top_k))
-        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
-        _same_device(h, ids=ids, logp=logp, stats=stats, top_ids=top_ids, top_logp=top_logp, status=status)
-        check("mls_token_logprobs",
-              lib().mls_token_logprobs(T, D, V, N, _ptr(ids), h.data_ptr(), W.data_ptr(), dt, _ptr(logp),
-                                       stats.data_ptr(), top_k, _ptr(top_ids), _ptr(top_logp), workspace.data_ptr(),
-                                       ws_bytes, _ptr(status), _stream_ptr(stream)))
+        N = _head_ids(ids, T, dev)
+    elif logp is not None:
+        raise ValueError("logp was given without ids")
+    if not top_k and (top_ids is not None or top_logp is not None):
+        raise ValueError("top_ids or top_logp was given without top_k")
+    nbytes = token_logprobs_workspace(T, D, V, N, top_k, h.dtype)[0]
+    if logp is not None:
+        _head_fit(logp, "logp", f32, ids.shape, dev)
+    elif N:
+        logp = torch.empty(ids.shape, dtype=f32, device=dev)
+    if stats is not None:
+        _head_fit(stats, "stats", f32, (2, T), dev)
+    else:
+        stats = torch.empty((2, T), dtype=f32, device=dev)
+    if top_ids is not None:
+        _head_fit(top_ids, "top_ids", torch.int32, (T, top_k), dev)
+    elif top_k:
+        top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if top_logp is not None:
+        _head_fit(top_logp, "top_logp", f32, (T, top_k), dev)
+    elif top_k:
+        top_logp = torch.empty((T, top_k), dtype=f32, device=dev)
+    if status is not None:
+        _head_fit(status, "status", torch.int32, status.shape, dev)
+    workspace, ws_bytes = _head_workspace(workspace, nbytes, dev)
+    check("mls_token_logprobs",
+          lib().mls_token_logprobs(T, D, V, N, _ptr(ids), h.data_ptr(), W.data_ptr(), dt, _ptr(logp),
+                                   stats.data_ptr(), top_k, _ptr(top_ids), _ptr(top_logp), workspace.data_ptr(),
+                                   ws_bytes, _ptr(status), _head_stream(stream, dev)))
     return logp, stats, top_ids, top_logp
 
 
+@functools.lru_cache(maxsize=1024)
 def token_logprobs_bwd_workspace(T: int, D: int, V: int, N: int, dtype: torch.dtype) -> Tuple[int, int]:
     """(bytes, smallest accepted bytes) of token_logprobs_bwd (see mls_token_logprobs_bwd_workspace)."""
     n, least = ctypes.c_size_t(), ctypes.c_size_t()
     check("mls_token_logprobs_bwd_workspace",
-          lib().mls_token_logprobs_bwd_workspace(T, D, V, N, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
-                                                 ctypes.byref(n), ctypes.byref(least)))
+          lib().mls_token_logprobs_bwd_workspace(T, D, V, N, _code_of(dtype), ctypes.byref(n), ctypes.byref(least)))
     return n.value, least.value
 
 
@@ -437,46 +464,51 @@ def token_logprobs_bwd(ids: torch.Tensor, h: torch.Tensor, W: torch.Tensor, stat
     """Gradients of token_logprobs' log probabilities (g_logp, the shape of ids) and entropies (g_entropy [T])
     with respect to h and W (see mls_token_logprobs_bwd).  Returns (dh or None, dW or None); dW is fp32, or
     bf16 with dW_dtype=torch.bfloat16."""
-    T, D, V, dt = _head_common(h, W)
-    _need(ids, "ids", torch.int32)
-    if ids.dim() not in (1, 2) or ids.shape[0] != T:
-        raise ValueError("ids must be [T] or [T, N]")
-    N = 1 if ids.dim() == 1 else ids.shape[1]
-    with torch.cuda.device(h.device):
-        nbytes, _ = token_logprobs_bwd_workspace(T, D, V, N, h.dtype)
-        _head_rows(stats, "stats", torch.float32, (2, T))
-        _head_rows(g_logp, "g_logp", torch.float32, ids.shape)
-        _head_rows(g_entropy, "g_entropy", torch.float32, (T,))
-        dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
-        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
-        _same_device(h, ids=ids, stats=stats, g_logp=g_logp, g_entropy=g_entropy, status=status)
-        check("mls_token_logprobs_bwd",
-              lib().mls_token_logprobs_bwd(T, D, V, N, ids.data_ptr(), h.data_ptr(), W.data_ptr(), dt,
-                                           stats.data_ptr(), g_logp.data_ptr(), _ptr(g_entropy), _ptr(dh), _ptr(dW),
-                                           dW_code, int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes,
-                                           _ptr(status), _stream_ptr(stream)))
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return token_logprobs_bwd(ids, h, W, stats, g_logp, g_entropy, dh=dh, dW=dW, dW_dtype=dW_dtype,
+                                      accumulate_dW=accumulate_dW, want_dh=want_dh, want_dW=want_dW,
+                                      workspace=workspace, status=status, stream=stream)
+    T, D, V, dt, dev = _head_common(h, W)
+    N = _head_ids(ids, T, dev)
+    _head_fit(stats, "stats", torch.float32, (2, T), dev)
+    _head_fit(g_logp, "g_logp", torch.float32, ids.shape, dev)
+    if g_entropy is not None:
+        _head_fit(g_entropy, "g_entropy", torch.float32, (T,), dev)
+    if status is not None:
+        _head_fit(status, "status", torch.int32, status.shape, dev)
+    dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
+    workspace, ws_bytes = _head_workspace(workspace, token_logprobs_bwd_workspace(T, D, V, N, h.dtype)[0], dev)
+    check("mls_token_logprobs_bwd",
+          lib().mls_token_logprobs_bwd(T, D, V, N, ids.data_ptr(), h.data_ptr(), W.data_ptr(), dt,
+                                       stats.data_ptr(), g_logp.data_ptr(), _ptr(g_entropy), _ptr(dh), _ptr(dW),
+                                       dW_code, int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes,
+                                       _ptr(status), _head_stream(stream, dev)))
     return dh, dW
 
 
+@functools.lru_cache(maxsize=1024)
 def topk_distill_workspace(T: int, D: int, V: int, K: int, dtype: torch.dtype) -> Tuple[int, int, int, int]:
     """(forward bytes, smallest, backward bytes, smallest) of the distillation (see mls_topk_distill_workspace)."""
     v = [ctypes.c_size_t() for _ in range(4)]
     check("mls_topk_distill_workspace",
-          lib().mls_topk_distill_workspace(T, D, V, K, MLS_BF16 if dtype == torch.bfloat16 else MLS_F32,
-                                           *[ctypes.byref(x) for x in v]))
+          lib().mls_topk_distill_workspace(T, D, V, K, _code_of(dtype), *[ctypes.byref(x) for x in v]))
     return tuple(x.value for x in v)
 
 
-def _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W):
-    T, D, V, dt = _head_common(h, W)
-    _need(teacher_ids, "teacher_ids", torch.int32, 2)
+def _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status):
+    T, D, V, dt, dev = _head_common(h, W)
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be [T, K]")
     K = teacher_ids.shape[1]
-    _head_rows(y, "y", torch.int32, (T,))
-    _head_rows(teacher_ids, "teacher_ids", torch.int32, (T, K))
-    _head_rows(teacher_logits, "teacher_logits", torch.float32, (T, K))
-    _head_rows(token_weights, "token_weights", torch.float32, (T,))
-    _same_device(h, y=y, teacher_ids=teacher_ids, teacher_logits=teacher_logits, token_weights=token_weights)
-    return T, D, V, K, dt
+    _head_fit(y, "y", torch.int32, (T,), dev)
+    _head_fit(teacher_ids, "teacher_ids", torch.int32, (T, K), dev)
+    _head_fit(teacher_logits, "teacher_logits", torch.float32, (T, K), dev)
+    if token_weights is not None:
+        _head_fit(token_weights, "token_weights", torch.float32, (T,), dev)
+    if status is not None:
+        _head_fit(status, "status", torch.int32, status.shape, dev)
+    return T, D, V, K, dt, dev
 
 
 def topk_distill_fwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, h: torch.Tensor,
@@ -487,22 +519,26 @@ def topk_distill_fwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
 
     Returns (losses [3] = mean cross-entropy, mean distillation term, their mix; stats [3, T] = log-sum-exp and
     the two terms of every token)."""
-    T, D, V, K, dt = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W)
-    with torch.cuda.device(h.device):
-        nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[0]
-        if losses is None:
-            losses = torch.empty(3, dtype=torch.float32, device=h.device)
-        if stats is None:
-            stats = torch.empty((3, T), dtype=torch.float32, device=h.device)
-        _head_rows(losses, "losses", torch.float32, (3,))
-        _head_rows(stats, "stats", torch.float32, (3, T))
-        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
-        _same_device(h, losses=losses, stats=stats, status=status)
-        check("mls_topk_distill_fwd",
-              lib().mls_topk_distill_fwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
-                                         _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
-                                         losses.data_ptr(), stats.data_ptr(), workspace.data_ptr(), ws_bytes,
-                                         _ptr(status), _stream_ptr(stream)))
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return topk_distill_fwd(y, teacher_ids, teacher_logits, h, W, alpha_d, token_weights=token_weights,
+                                    losses=losses, stats=stats, workspace=workspace, status=status, stream=stream)
+    T, D, V, K, dt, dev = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status)
+    nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[0]
+    if losses is not None:
+        _head_fit(losses, "losses", torch.float32, (3,), dev)
+    else:
+        losses = torch.empty(3, dtype=torch.float32, device=dev)
+    if stats is not None:
+        _head_fit(stats, "stats", torch.float32, (3, T), dev)
+    else:
+        stats = torch.empty((3, T), dtype=torch.float32, device=dev)
+    workspace, ws_bytes = _head_workspace(workspace, nbytes, dev)
+    check("mls_topk_distill_fwd",
+          lib().mls_topk_distill_fwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+                                     _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
+                                     losses.data_ptr(), stats.data_ptr(), workspace.data_ptr(), ws_bytes,
+                                     _ptr(status), _head_stream(stream, dev)))
     return losses, stats
 
 
@@ -513,19 +549,22 @@ def topk_distill_bwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
                      want_dW: bool = True, workspace=None, status=None, stream=None):
     """Gradients of topk_distill_fwd's mixed loss times grad_scale with respect to h and W (see
     mls_topk_distill_bwd).  Returns (dh or None, dW or None)."""
-    T, D, V, K, dt = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W)
-    with torch.cuda.device(h.device):
-        nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[2]
-        _head_rows(stats, "stats", torch.float32, (3, T))
-        dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
-        workspace, ws_bytes = _head_workspace(workspace, nbytes, h)
-        _same_device(h, stats=stats, status=status)
-        check("mls_topk_distill_bwd",
-              lib().mls_topk_distill_bwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
-                                         _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
-                                         stats.data_ptr(), float(grad_scale), _ptr(dh), _ptr(dW), dW_code,
-                                         int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes, _ptr(status),
-                                         _stream_ptr(stream)))
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return topk_distill_bwd(y, teacher_ids, teacher_logits, h, W, stats, alpha_d, grad_scale,
+                                    token_weights=token_weights, dh=dh, dW=dW, dW_dtype=dW_dtype,
+                                    accumulate_dW=accumulate_dW, want_dh=want_dh, want_dW=want_dW,
+                                    workspace=workspace, status=status, stream=stream)
+    T, D, V, K, dt, dev = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status)
+    _head_fit(stats, "stats", torch.float32, (3, T), dev)
+    dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
+    workspace, ws_bytes = _head_workspace(workspace, topk_distill_workspace(T, D, V, K, h.dtype)[2], dev)
+    check("mls_topk_distill_bwd",
+          lib().mls_topk_distill_bwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+                                     _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
+                                     stats.data_ptr(), float(grad_scale), _ptr(dh), _ptr(dW), dW_code,
+                                     int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes, _ptr(status),
+                                     _head_stream(stream, dev)))
     return dh, dW
 
 

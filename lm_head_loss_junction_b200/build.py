@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmls.so")
 SOURCES = ["api.cu", "junction.cu", "segsum.cu", "loss_simt.cu", "loss_tc.cu", "junction_noalloc.cu",
-           "head_api.cu", "head_tc.cu", "head_rows.cu", "head_simt.cu"]
+           "head_api.cu", "head_tc.cu", "head_few.cu", "head_rows.cu", "head_simt.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

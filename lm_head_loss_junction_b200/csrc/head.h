@@ -117,6 +117,10 @@ struct HeadForward {
 };
 cudaError_t head_tc_forward(const HeadProblem& p, const HeadForward& f, cudaStream_t st);
 
+// The same for at most kFewTokens tokens, logits always written (f.logits != NULL).
+constexpr int64_t kFewTokens = 128;
+cudaError_t head_tc_few(const HeadProblem& p, const HeadForward& f, cudaStream_t st);
+
 // dh and dW (either may be NULL) from the entries, one chunk of the vocabulary at a time.
 size_t head_tc_bwd_bytes(const HeadProblem& p, int64_t Vc);
 int64_t head_tc_bwd_chunk(const HeadProblem& p, size_t budget);

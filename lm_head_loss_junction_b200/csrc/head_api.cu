@@ -60,7 +60,7 @@ HeadProblem shape(int64_t T, int64_t D, int64_t V, mls_dtype dt) {
 // of Tb tokens' [partial statistics][picked logits][logits].
 struct ForwardPlan {
   int64_t Tb, ld;
-  bool store;                      // the logits are written (alternatives, or fp32)
+  bool store;                      // the logits are written (alternatives, few tokens, or fp32)
   size_t entries, terms, part, picked, logits;
   size_t total() const { return entries + terms + part + picked + logits; }
 };
@@ -69,7 +69,7 @@ ForwardPlan forward_plan(const HeadProblem& p, int Ntot, int K, bool distill, in
   ForwardPlan f{};
   f.Tb = Tb;
   f.ld = (p.V + 63) / 64 * 64;
-  f.store = K > 0 || !p.bf16;
+  f.store = K > 0 || !p.bf16 || p.T <= mls::kFewTokens;
   f.entries = f.store ? 0 : mls::head_entries_bytes(p.T, p.V, Ntot, false);
   f.terms = distill ? head_align(static_cast<size_t>(p.T) * 3 * sizeof(float)) : 0;
   f.part = head_align(static_cast<size_t>(Tb) * head_splits(p.V) * sizeof(HeadPart));
@@ -148,7 +148,7 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
       }
       w.ld_first = p.T;
       w.picked = picked;
-      err = mls::head_tc_forward(p, w, st);
+      err = p.T <= mls::kFewTokens ? mls::head_tc_few(p, w, st) : mls::head_tc_forward(p, w, st);
     } else {
       err = mls::head_simt_logits(p, t0, n, logits, plan.ld, part, st);
     }

@@ -15,10 +15,11 @@ constexpr unsigned kFull = 0xffffffffu;
 // ------------------------------------------------------------------ entry lists
 // One warp per token turns the token's ids into a list sorted by id (ties by
 // position), with the position (forward) or the coefficient over the row scale
-// (backward); then the first entry of every split, one lane per token so that
-// the bytes of 32 tokens are written together.  A few microseconds: the table
-// of one byte per token and split is what it writes most.
-constexpr int kEntryTokens = 32;
+// (backward); then the block's threads write the first entry of every split,
+// eight tokens' bytes together.  Bound by the latency of its few dependent
+// steps, so a token is a warp's only one (four in turn, with 32 lanes along the
+// tokens in the table, took four times as long).
+constexpr int kEntryTokens = 8;
 constexpr int kMaxTot = kMaxEntries + 1;
 constexpr int kPerLane = (kMaxTot + 31) / 32;
 
@@ -41,9 +42,9 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kEntryTokens;
   const int N = in.N, tot = out.Ntot;
-  for (int i = warp; i < kEntryTokens; i += 8) {
+  const int i = warp;
+  if (t0 + i < in.T) {
     const int64_t t = t0 + i;
-    if (t >= in.T) break;
     int id[kPerLane];
     float c[kPerLane];
     bool there[kPerLane];
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
       const int j = k * 32 + lane;
       if (!there[k]) continue;
       int rank = 0;
+#pragma unroll 8
       for (int o = 0; o < tot; ++o) {
         const int other = s.id[i][o];
         rank += other < id[k] || (other == id[k] && o < j);
@@ -140,15 +142,16 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
     }
   }
   __syncthreads();
-  const int64_t t = t0 + lane;
+  const int own = threadIdx.x % kEntryTokens;
+  const int64_t t = t0 + own;
   if (t < in.T) {
-    const int n = s.count[lane];
-    for (int sp = warp; sp <= n_splits; sp += 8) {
+    const int n = s.count[own];
+    for (int sp = threadIdx.x / kEntryTokens; sp <= n_splits; sp += 256 / kEntryTokens) {
       const int64_t edge = static_cast<int64_t>(sp) * kHeadSplit;
       int lo = 0, hi = n;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (s.sorted[lane][mid] < edge) lo = mid + 1; else hi = mid;
+        if (s.sorted[own][mid] < edge) lo = mid + 1; else hi = mid;
       }
       out.first[static_cast<int64_t>(sp) * in.T + t] = static_cast<uint8_t>(lo);
     }
@@ -292,10 +295,9 @@ __device__ __forceinline__ uint64_t top_key(float v, uint32_t index) {
   return static_cast<uint64_t>(ordered(v)) << 32 | ~index;
 }
 
-constexpr int kTopThreads = 256;
-
 // The k-th largest of n distinct keys (1 <= k <= n) as a lower bound: exactly k
-// keys are at or above the returned value.  All threads of the block call it.
+// keys are at or above the returned value.  All kTopThreads threads of the block call it.
+template <int kTopThreads>
 __device__ uint64_t select_kth(const uint64_t* keys, int n, int k, int* hist, int* chosen) {
   uint64_t prefix = 0;
   int shift = 56;
@@ -344,44 +346,82 @@ __device__ uint64_t select_kth(const uint64_t* keys, int n, int k, int* hist, in
   return prefix;
 }
 
-template <bool BF16>
-__device__ __forceinline__ double dot64(const void* h, const void* w, int64_t D, int lane) {
-  double acc = 0.0;
-  if (BF16) {
+// Products h . W[id[g]] in 64 bits of G rows of W at once (their loads in
+// flight together), by one warp; lane 0's results count.
+template <bool BF16, int G>
+__device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, const int* id, int lane,
+                                       double (&acc)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) acc[g] = 0.0;
+  if constexpr (BF16) {
     // a product of two bf16 values is exact in fp32
     const uint4* a = static_cast<const uint4*>(h);
-    const uint4* b = static_cast<const uint4*>(w);
-    for (int64_t i = lane; i < D / 8; i += 32) {
-      float x[8], y[8];
-      bf16x8_to_f32(__ldg(a + i), x);
-      bf16x8_to_f32(__ldg(b + i), y);
+    const uint4* b[G];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc += static_cast<double>(x[k] * y[k]);
+    for (int g = 0; g < G; ++g) b[g] = static_cast<const uint4*>(W) + id[g] * (D / 8);
+    const int n = static_cast<int>(D / 8);
+#pragma unroll(G == 1 ? 4 : 1)
+    for (int i = lane; i < n; i += 32) {
+      uint4 w[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) w[g] = __ldg(b[g] + i);
+      float x[8];
+      bf16x8_to_f32(__ldg(a + i), x);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float y[8];
+        bf16x8_to_f32(w[g], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[g] += static_cast<double>(x[k] * y[k]);
+      }
     }
   } else {
     const float* a = static_cast<const float*>(h);
-    const float* b = static_cast<const float*>(w);
-    for (int64_t i = lane; i < D; i += 32) acc = fma(static_cast<double>(a[i]), static_cast<double>(b[i]), acc);
+    for (int64_t i = lane; i < D; i += 32) {
+      const double x = __ldg(a + i);
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[g] = fma(x, static_cast<double>(__ldg(static_cast<const float*>(W) + id[g] * D + i)), acc[g]);
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-  return acc;
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(kFull, acc[g], o);
+}
+
+// val[i] = h . W[id[i]] for i < n, by the block's warps.
+template <bool BF16, int G>
+__device__ __forceinline__ void block_dots(const void* h, const void* W, int64_t D, const int* id, int n, double* val,
+                                           int warp, int warps, int lane) {
+  for (int i = warp * G; i < n; i += warps * G) {
+    int own[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) own[g] = id[i + g < n ? i + g : n - 1];
+    double acc[G];
+    dots64<BF16, G>(h, W, D, own, lane, acc);
+    if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (i + g < n) val[i + g] = acc[g];
+    }
+  }
 }
 
 struct TopSmem {
   int hist[256];
   int chosen[4];
-  float part[kTopThreads / 32][3];
+  float part[32][3];
+  uint32_t least[32];
   int count;
   int n_sel;
   int sel[kMaxEntries + kTopMore];
   uint64_t fin[kMaxEntries + kTopMore];
-  double fine[kMaxEntries + kTopMore];
-  double given[kMaxEntries];
+  int id[2 * kMaxEntries + kTopMore];        // the candidates, then the given tokens
+  double fine[2 * kMaxEntries + kTopMore];   // their logits in 64 bits
   float dz[kMaxEntries + kTopMore], du[kMaxEntries + kTopMore];   // by rank: a fixed order of summation
 };
 
-template <bool BF16>
+template <bool BF16, int kTopThreads>
 __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C) {
   extern __shared__ uint8_t raw[];
   TopSmem& s = *reinterpret_cast<TopSmem*>(raw);
@@ -412,7 +452,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   // the splits that hold the candidates, and a lower bound on the C-th largest logit
   const int n_take = n_splits < C ? n_splits : C;
   uint64_t bound = 0;
-  if (n_splits > C) bound = select_kth(keys, n_splits, C, s.hist, s.chosen);
+  if (n_splits > C) bound = select_kth<kTopThreads>(keys, n_splits, C, s.hist, s.chosen);
   uint32_t least = 0xffffffffu;
   for (int i = threadIdx.x; i < n_splits; i += kTopThreads)
     if (keys[i] >= bound) {
@@ -420,10 +460,10 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
       least = min(least, static_cast<uint32_t>(keys[i] >> 32));
     }
   least = __reduce_min_sync(kFull, least);
-  if (lane == 0) s.hist[warp] = static_cast<int>(least);
+  if (lane == 0) s.least[warp] = least;
   __syncthreads();
   if (n_splits > C) {
-    for (int i = 0; i < kTopThreads / 32; ++i) least = min(least, static_cast<uint32_t>(s.hist[i]));
+    for (int i = 0; i < kTopThreads / 32; ++i) least = min(least, s.least[i]);
   } else {
     least = 0;
   }
@@ -442,33 +482,34 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   __syncthreads();
   const int n = s.count;
   uint64_t last = 0;
-  if (n > C) last = select_kth(keys, n, C, s.hist, s.chosen);
+  if (n > C) last = select_kth<kTopThreads>(keys, n, C, s.hist, s.chosen);
   if (threadIdx.x == 0) s.n_sel = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kTopThreads)
     if (keys[i] >= last) s.fin[atomicAdd(&s.n_sel, 1)] = keys[i];
   __syncthreads();
 
-  // ranked by their products in 64 bits (fewer than C only where logits are not numbers)
+  // their logits and the given tokens' as products in 64 bits (fewer than C only where logits are not numbers)
   const int have = s.n_sel < C ? s.n_sel : C;
-  const size_t esize = BF16 ? 2 : 4;
-  const char* hrow = static_cast<const char*>(f.h) + t * f.D * esize;
-  for (int i = warp; i < have; i += kTopThreads / 32) {
-    const int64_t id = static_cast<int64_t>(~static_cast<uint32_t>(s.fin[i]));
-    const double v = dot64<BF16>(hrow, static_cast<const char*>(f.W) + id * f.D * esize, f.D, lane);
-    if (lane == 0) s.fine[i] = v;
+  if (threadIdx.x < have) s.id[threadIdx.x] = static_cast<int>(~static_cast<uint32_t>(s.fin[threadIdx.x]));
+  if (threadIdx.x < f.N) {
+    const int id = f.ids[t * f.N + threadIdx.x];
+    s.id[have + threadIdx.x] = id >= 0 && id < f.V ? id : 0;
   }
-  for (int j = warp; j < f.N; j += kTopThreads / 32) {
-    const int id = f.ids[t * f.N + j];
-    if (id < 0 || id >= f.V) continue;
-    const double v = dot64<BF16>(hrow, static_cast<const char*>(f.W) + static_cast<int64_t>(id) * f.D * esize, f.D, lane);
-    if (lane == 0) s.given[j] = v;
+  __syncthreads();
+  {
+    constexpr int kWarps = kTopThreads / 32;
+    const char* hrow = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
+    const int items = have + f.N;
+    if (items <= kWarps) block_dots<BF16, 1>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+    else if (items <= 3 * kWarps) block_dots<BF16, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+    else block_dots<BF16, 6>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
   }
   __syncthreads();
   int rank = kMaxEntries + kTopMore;
   uint32_t id = 0;
   if (threadIdx.x < have) {
-    id = ~static_cast<uint32_t>(s.fin[threadIdx.x]);
+    id = s.id[threadIdx.x];
     // doubles as ordered integers, so that every value (a NaN too) has one rank
     auto order = [](double d) {
       const int64_t b = __double_as_longlong(d + 0.0);
@@ -478,7 +519,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     rank = 0;
     for (int i = 0; i < have; ++i) {
       const uint64_t other = order(s.fine[i]);
-      rank += other > mine || (other == mine && ~static_cast<uint32_t>(s.fin[i]) < id);
+      rank += other > mine || (other == mine && static_cast<uint32_t>(s.id[i]) < id);
     }
     const float was = unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)) - m;
     const float is = static_cast<float>(s.fine[threadIdx.x] - m);
@@ -496,7 +537,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   du = warp_sum(du);
   z += dz;
   const float logz = logf(z);
-  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.given);
+  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.fine + have);
   if (rank < f.K) {
     f.top_ids[t * f.K + rank] = static_cast<int32_t>(id);
     f.top_logp[t * f.K + rank] = static_cast<float>(s.fine[threadIdx.x] - m) - logz;
@@ -556,10 +597,14 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const size_t list = static_cast<size_t>(take) * kHeadSplit;
   const size_t n = list > static_cast<size_t>(f.n_splits) ? list : static_cast<size_t>(f.n_splits);
   const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + n * sizeof(uint64_t);
-  auto fn = f.bf16 ? head_top_kernel<true> : head_top_kernel<false>;
+  // Few tokens leave SMs idle: their blocks get all the warps that help.  (T = 1, D = 2304, K = 8: 24 us with 256
+  // threads.)  Many tokens share an SM: 256 threads, several blocks.
+  const bool wide = f.T <= 148;
+  auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : head_top_kernel<true, 256>)
+                   : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 256>);
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  fn<<<static_cast<unsigned>(f.T), kTopThreads, smem, st>>>(f, C);
+  fn<<<static_cast<unsigned>(f.T), wide ? 1024 : 256, smem, st>>>(f, C);
   note_launches(1);
   return cudaGetLastError();
 }

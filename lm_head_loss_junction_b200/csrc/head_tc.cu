@@ -27,6 +27,7 @@
 #include <mutex>
 
 #include "head.h"
+#include "head_host.h"
 #include "umma.cuh"
 
 namespace mls {
@@ -40,12 +41,100 @@ constexpr int kUK = 16;                  // K per tcgen05.mma
 constexpr int kStages = 6;               // 32 KB per stage and CTA
 constexpr int kEpiWarps = 8;             // two per TMEM lane quadrant, 128 columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kCopyThreads = 64;         // two more warps: as many registers per thread as without them
 constexpr int kStageRow = 80;            // bytes of a staged row of 32 fp16 (padded against bank conflicts)
 constexpr int kGroupM = 8;               // row tiles per raster group: they share their A panels in L2
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMasked = -3.0e38f;      // logit of a column past V: finite, so that 0 * it is 0
 
 enum Epi { kStats, kLogits, kGrad, kDh, kDw };
+
+// ------------------------------------------------------------------ fp16 operand copies
+// dst[r][:] = fp16(src[r][:] * f_r), f_r = 1, or 64 times the row's scale over
+// the largest one (64: rows down to 2^-20 of the largest scale stay in fp16's
+// normal range at values near 1, values up to 512 do not pass it); tracks the largest magnitude.  kind::f16 takes A and B of one
+// type, so G' in fp16 needs W and h in fp16.  bf16's 8 significant bits fit in
+// fp16's 11: values in its normal range convert exactly.
+struct CopyArgs {
+  const uint4* src;
+  uint4* dst;
+  int64_t n_vec;
+  int vec_per_row;
+  const float4* row;               // row scales in .w (NULL: 1)
+  const unsigned int* smax;
+  unsigned int* maxbits;
+  float* inv;
+};
+
+__device__ __forceinline__ uint4 to_half8(const uint4& v, float f, float& mx) {
+  float x[8];
+  bf16x8_to_f32(v, x);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    // a row of scale 0 is left out, whatever it holds
+    const float lo = f == 0.f ? 0.f : x[2 * k] * f, hi = f == 0.f ? 0.f : x[2 * k + 1] * f;
+    mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
+    __half2 h = __floats2half2_rn(lo, hi);
+    w[k] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr float kRowLift = 64.f;
+
+__device__ __forceinline__ float copy_factor(const CopyArgs& a, int64_t i, float smax) {
+  if (a.row == nullptr) return 1.f;
+  return smax > 0.f ? a.row[i / a.vec_per_row].w / smax * kRowLift : 0.f;
+}
+
+// Thread `first` of `stride` threads.
+__device__ __forceinline__ void copy_part(const CopyArgs& a, int64_t first, int64_t stride) {
+  if (a.n_vec == 0) return;
+  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
+  float mx = 0.f;
+  int64_t i = first;
+  for (; i + 3 * stride < a.n_vec; i += 4 * stride) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __ldg(a.src + i + k * stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
+  }
+  for (; i < a.n_vec; i += stride) a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax), mx);
+  mx = warp_max(mx);
+  if ((threadIdx.x & 31) == 0 && mx > 0.f) atomicMax(a.maxbits, __float_as_uint(mx));
+}
+
+struct CopyJobs {
+  CopyArgs w, h;
+};
+
+__global__ void __launch_bounds__(256) head_copy_kernel(const CopyJobs jobs) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  copy_part(blockIdx.y == 0 ? jobs.w : jobs.h, first, static_cast<int64_t>(gridDim.x) * blockDim.x);
+}
+
+// The copy again with a power-of-two scale when the largest magnitude is at or
+// past 2^15 or below 2^-10; the reciprocal of the scale for the epilogue.
+__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyJobs jobs) {
+  const CopyArgs& a = blockIdx.y == 0 ? jobs.w : jobs.h;
+  if (a.n_vec == 0) return;
+  const float mx = __uint_as_float(*a.maxbits);
+  float s = 1.f;
+  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 1024.f))) {
+    int e = 13 - ilogbf(mx);
+    e = e < -126 ? -126 : (e > 126 ? 126 : e);
+    s = ldexpf(1.f, e);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
+  if (s == 1.f) return;
+  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
+  float unused = 0.f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.n_vec; i += stride)
+    a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax) * s, unused);
+}
 
 struct TileMaps {
   CUtensorMap a, b;
@@ -54,7 +143,9 @@ struct TileMaps {
 struct TileArgs {
   int rows, cols;                  // extents of the output
   int kblocks;
-  int n_mt, tiles;                 // 256-row tiles, all tiles
+  int n_mt, n_nt;                  // tiles down and across
+  int parts, part_kblocks;         // K in parts (dh only): each part's tiles are units of their own
+  int units;
   // stats, logits, grad
   int v0;                          // vocabulary id of column 0
   int n_splits;                    // splits of a row of part
@@ -75,7 +166,13 @@ struct TileArgs {
   int accumulate;
   const float* inv;                // device: 1 / scale of the fp16 copy
   const unsigned int* smax;        // device: largest row scale (dw)
+  CopyJobs copy;                   // grad: fp16 copies made by two more warps
   int32_t* status;
+};
+
+// What one turn of a CTA pair computes: a tile over kblocks [kb0, kb1).
+struct Unit {
+  int mt, nt, part, kb0, kb1;
 };
 
 struct __align__(1024) TileSmem {
@@ -96,14 +193,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void tile_at(const TileArgs& a, int n_nt, int i, int& mt, int& nt) {
-  const int per_group = kGroupM * n_nt;
+__device__ __forceinline__ Unit unit_at(const TileArgs& a, int i) {
+  Unit u;
+  const int tiles = a.n_mt * a.n_nt;
+  u.part = i / tiles;
+  i -= u.part * tiles;
+  const int per_group = kGroupM * a.n_nt;
   const int g = i / per_group;
   const int first = g * kGroupM;
   const int gm = min(kGroupM, a.n_mt - first);
   const int r = i - g * per_group;
-  nt = r / gm;
-  mt = first + r % gm;
+  u.nt = r / gm;
+  u.mt = first + r % gm;
+  u.kb0 = u.part * a.part_kblocks;
+  u.kb1 = min(a.kblocks, u.kb0 + a.part_kblocks);
+  return u;
 }
 
 __device__ __forceinline__ uint32_t pack_g2(float lo, float hi) {
@@ -155,7 +259,7 @@ struct Layout {
 
 template <Epi EPI, bool OUT_BF16>
 __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_t acc_col, int warp, int lane,
-                                         int64_t row, int col_tile, int half, uint64_t* tempty) {
+                                         int64_t row, int col_tile, int half, int part, uint64_t* tempty) {
   const bool valid = row < a.rows;
   const int c0 = col_tile + half * 128;
   auto release = [&]() {
@@ -308,7 +412,8 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
           dst[k] = f32_to_bf16x8(f);
         }
       } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + off);
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
+                                                static_cast<int64_t>(part) * a.rows * a.cols + off);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           float4 v = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
@@ -326,8 +431,11 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
   }
 }
 
+template <Epi EPI>
+constexpr int threads_of() { return EPI == kGrad ? kThreads + kCopyThreads : kThreads; }
+
 template <Epi EPI, bool OUT_BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1)
     head_tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs a) {
   using L = Layout<EPI>;
   extern __shared__ uint8_t smem_raw[];
@@ -338,7 +446,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int n_nt = a.tiles / a.n_mt;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -370,12 +477,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int tile = pair; tile < a.tiles && ok; tile += npairs) {
-        int mt, nt;
-        tile_at(a, n_nt, tile, mt, nt);
-        const int row0 = mt * 2 * kBM + static_cast<int>(rank) * kBM;      // this CTA's rows of A
-        const int n0 = nt * kBN + static_cast<int>(rank) * (kBN / 2);      // and of B
-        for (int kb = 0; kb < a.kblocks; ++kb) {
+      for (int i = pair; i < a.units && ok; i += npairs) {
+        const Unit u = unit_at(a, i);
+        const int row0 = u.mt * 2 * kBM + static_cast<int>(rank) * kBM;    // this CTA's rows of A
+        const int n0 = u.nt * kBN + static_cast<int>(rank) * (kBN / 2);    // and of B
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait(&s.empty[stage], phase ^ 1, abort, a.status)) { ok = false; break; }
           const uint32_t lfull = mapa_shared(smem_u32(&s.full[stage]), 0);
           if (leader) mbar_arrive_expect_tx(&s.full[stage], 2 * (kBM + kBN / 2) * kBK * 2);
@@ -415,12 +521,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t b_lbo = L::b_mn ? 64 * kBK * 2 : 16;
       uint32_t stage = 0, phase = 0, iter = 0;
       bool ok = true;
-      for (int tile = pair; tile < a.tiles && ok; tile += npairs, ++iter) {
+      for (int i = pair; i < a.units && ok; i += npairs, ++iter) {
+        const Unit u = unit_at(a, i);
         const uint32_t buf = iter & 1;
         if (!mbar_wait(&s.tempty[buf], ((iter >> 1) & 1) ^ 1, abort, a.status)) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * kBN;
-        for (int kb = 0; kb < a.kblocks; ++kb) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait(&s.full[stage], phase, abort, a.status)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = smem_desc_sw128(smem_u32(s.a[stage]), a_lbo, 1024);
@@ -428,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBK / kUK; ++k)
             umma_bf16_pair(d, da + static_cast<uint64_t>(k * a_step), db + static_cast<uint64_t>(k * b_step), idesc,
-                           (kb | k) != 0);
+                           kb > u.kb0 || k > 0);
           const uint32_t e = smem_u32(&s.empty[stage]);
           umma_commit_pair(mapa_shared(e, 0));
           umma_commit_pair(mapa_shared(e, 1));
@@ -444,21 +551,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int dummy = 0;
       (void)mbar_wait(&s.drain, 0, &dummy, a.status);     // every MMA done before TMEM is released
     }
-  } else {
+  } else if (warp < 2 + kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;                               // TMEM lane quadrant this warp may read
     const int half = (warp - 2) >> 2;
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     uint32_t iter = 0;
-    for (int tile = pair; tile < a.tiles; tile += npairs, ++iter) {
-      int mt, nt;
-      tile_at(a, n_nt, tile, mt, nt);
+    for (int i = pair; i < a.units; i += npairs, ++iter) {
+      const Unit u = unit_at(a, i);
       const uint32_t buf = iter & 1;
       if (!warp_wait(&s.tfull[buf], (iter >> 1) & 1, abort, a.status)) break;
       tc_fence_after();
-      const int64_t row = static_cast<int64_t>(mt) * 2 * kBM + rank * kBM + q * 32 + lane;
-      epilogue<EPI, OUT_BF16>(a, s, base + buf * kBN, warp, lane, row, nt * kBN, half, &s.tempty[buf]);
+      const int64_t row = static_cast<int64_t>(u.mt) * 2 * kBM + rank * kBM + q * 32 + lane;
+      epilogue<EPI, OUT_BF16>(a, s, base + buf * kBN, warp, lane, row, u.nt * kBN, half, u.part, &s.tempty[buf]);
     }
+  } else if constexpr (EPI == kGrad) {
+    // ---------------------------------------------------------------- fp16 copies for dh and dw
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x - kThreads;
+    copy_part(a.copy.w, first, static_cast<int64_t>(gridDim.x) * kCopyThreads);
+    copy_part(a.copy.h, first, static_cast<int64_t>(gridDim.x) * kCopyThreads);
   }
 
   __syncthreads();
@@ -471,79 +582,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ fp16 operand copies
-// dst[r][:] = fp16(src[r][:] * f_r), f_r = 1, or 64 times the row's scale over
-// the largest one (64: rows down to 2^-20 of the largest scale stay in fp16's
-// normal range at values near 1, values up to 512 do not pass it); tracks the largest magnitude.  kind::f16 takes A and B of one
-// type, so G' in fp16 needs W and h in fp16.  bf16's 8 significant bits fit in
-// fp16's 11: values in its normal range convert exactly.
-struct CopyArgs {
-  const uint4* src;
-  uint4* dst;
-  int64_t n_vec;
+// dh from the parts of a split K, summed in order: into acc, or with acc (may
+// be NULL) times the row's scale to bf16.
+struct ReduceArgs {
+  const float4* part;              // [parts][n] of four values
+  int parts;
+  int64_t n;
   int vec_per_row;
-  const float4* row;               // row scales in .w (NULL: 1)
-  const unsigned int* smax;
-  unsigned int* maxbits;
-  float* inv;
+  float4* acc;
+  int acc_in;                      // acc holds earlier chunks
+  const float4* row;
+  uint2* out;                      // bf16, or NULL: the sums go to acc
 };
 
-__device__ __forceinline__ uint4 to_half8(const uint4& v, float f, float& mx) {
-  float x[8];
-  bf16x8_to_f32(v, x);
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    // a row of scale 0 is left out, whatever it holds
-    const float lo = f == 0.f ? 0.f : x[2 * k] * f, hi = f == 0.f ? 0.f : x[2 * k + 1] * f;
-    mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
-    __half2 h = __floats2half2_rn(lo, hi);
-    w[k] = *reinterpret_cast<uint32_t*>(&h);
+__global__ void __launch_bounds__(256) head_reduce_kernel(const ReduceArgs a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= a.n) return;
+  float4 v = a.acc_in ? a.acc[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    const float4 x = __ldg(a.part + p * a.n + i);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-constexpr float kRowLift = 64.f;
-
-__device__ __forceinline__ float copy_factor(const CopyArgs& a, int64_t i, float smax) {
-  if (a.row == nullptr) return 1.f;
-  return smax > 0.f ? a.row[i / a.vec_per_row].w / smax * kRowLift : 0.f;
-}
-
-__global__ void __launch_bounds__(256) head_copy_kernel(const CopyArgs a) {
-  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
-  float mx = 0.f;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (; i + 3 * stride < a.n_vec; i += 4 * stride) {
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldg(a.src + i + k * stride);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
+  if (a.out == nullptr) {
+    a.acc[i] = v;
+    return;
   }
-  for (; i < a.n_vec; i += stride) a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax), mx);
-  mx = warp_max(mx);
-  if ((threadIdx.x & 31) == 0 && mx > 0.f) atomicMax(a.maxbits, __float_as_uint(mx));
-}
-
-// The copy again with a power-of-two scale when the largest magnitude is at or
-// past 2^15 or below 2^-10; the reciprocal of the scale for the epilogue.
-__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyArgs a) {
-  const float mx = __uint_as_float(*a.maxbits);
-  float s = 1.f;
-  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 1024.f))) {
-    int e = 13 - ilogbf(mx);
-    e = e < -126 ? -126 : (e > 126 ? 126 : e);
-    s = ldexpf(1.f, e);
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
-  if (s == 1.f) return;
-  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
-  float unused = 0.f;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.n_vec; i += stride)
-    a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax) * s, unused);
+  const float s = a.row[i / a.vec_per_row].w;
+  a.out[i] = make_uint2(pack_bf16x2(v.x * s, v.y * s), pack_bf16x2(v.z * s, v.w * s));
 }
 
 // ------------------------------------------------------------------ host side
@@ -564,10 +633,18 @@ EncodeTiledFn get_encoder() {
   return fn;
 }
 
-// 2-D tensor of 16-bit elements [outer][ld], the first `inner` of each row
-// addressable (elements outside read as zero), 128-byte swizzled boxes.
-bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-              int box_outer, bool fp16) {
+constexpr int kMaxDevices = 64;
+
+int current_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) (void)cudaGetLastError();
+  return dev;
+}
+
+}  // namespace
+
+bool head_make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+                   int box_outer, bool fp16) {
   EncodeTiledFn enc = get_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
@@ -580,22 +657,33 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int num_sms() {
-  int dev = 0, n = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+int head_num_sms() {
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  int n = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 148;
+    if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
 }
+
+namespace {
 
 constexpr size_t kSmemBytes = sizeof(TileSmem) + 1024;
 
 // CTA pairs that can be resident at once: a persistent grid larger than that
-// would leave whole pairs waiting for a second wave.
-template <typename Kernel>
-int resident_pairs(Kernel fn) {
+// would leave whole pairs waiting for a second wave.  Asked once per kernel and
+// device (a property of both): the query costs the host more than a launch.
+template <Epi EPI, bool OUT_BF16>
+int resident_pairs() {
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  if (dev < kMaxDevices && known[dev].load(std::memory_order_relaxed) > 0)
+    return known[dev].load(std::memory_order_relaxed);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms()));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(head_num_sms()));
+  cfg.blockDim = dim3(threads_of<EPI>());
   cfg.dynamicSmemBytes = kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -605,37 +693,64 @@ int resident_pairs(Kernel fn) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, head_tile_kernel<EPI, OUT_BF16>, &cfg) != cudaSuccess || n <= 0) {
     (void)cudaGetLastError();
-    n = num_sms() / 2;
+    return head_num_sms() / 2;
   }
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
+int tiles_of(int64_t extent, int64_t tile) { return static_cast<int>((extent + tile - 1) / tile); }
+
+// parts: how many parts K is cut into (dh).
 template <Epi EPI, bool OUT_BF16>
-cudaError_t run_tiles(const TileMaps& maps, TileArgs a, int64_t kdim, cudaStream_t st) {
-  const int64_t n_mt = (a.rows + 2 * kBM - 1) / (2 * kBM);
-  const int64_t wide = EPI == kGrad ? a.gcols : a.cols;
-  const int64_t tiles = n_mt * ((wide + kBN - 1) / kBN);
-  if (tiles > INT32_MAX - 1024) return cudaErrorInvalidValue;
-  a.n_mt = static_cast<int>(n_mt);
-  a.tiles = static_cast<int>(tiles);
-  a.kblocks = static_cast<int>((kdim + kBK - 1) / kBK);
+cudaError_t run_tiles(const TileMaps& maps, TileArgs a, int64_t kdim, int parts, cudaStream_t st) {
+  a.n_mt = tiles_of(a.rows, 2 * kBM);
+  a.n_nt = tiles_of(EPI == kGrad ? a.gcols : a.cols, kBN);
+  a.kblocks = tiles_of(kdim, kBK);
+  a.part_kblocks = tiles_of(a.kblocks, parts);
+  a.parts = tiles_of(a.kblocks, a.part_kblocks);
+  const int64_t units = static_cast<int64_t>(a.n_mt) * a.n_nt * a.parts;
+  if (units > INT32_MAX - 1024) return cudaErrorInvalidValue;
+  a.units = static_cast<int>(units);
   auto fn = head_tile_kernel<EPI, OUT_BF16>;
   cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (err != cudaSuccess) return err;
-  const int resident = resident_pairs(fn);
-  const int pairs = a.tiles < resident ? a.tiles : resident;
-  fn<<<2 * pairs, kThreads, kSmemBytes, st>>>(maps, a);
+  const int resident = resident_pairs<EPI, OUT_BF16>();
+  const int pairs = a.units < resident ? a.units : resident;
+  fn<<<2 * pairs, threads_of<EPI>(), kSmemBytes, st>>>(maps, a);
   note_launches(1);
   return cudaGetLastError();
 }
 
-cudaError_t run_copy(const void* src, __half* dst, int64_t rows, int64_t D, const HeadEntries* scaled,
-                     unsigned int* maxbits, float* inv, cudaStream_t st) {
-  cudaError_t err = cudaMemsetAsync(maxbits, 0, sizeof(unsigned int), st);
-  if (err != cudaSuccess) return err;
-  CopyArgs a{};
+// Parts of dh's K: dh has ceil(T / 256) ceil(D / 256) tiles, few when T is
+// small, and K = V is long.  The count with the least of (turns of the pairs x
+// K per turn at 0.3 us per 64) + (the parts' fp32 sums, written and read, at
+// 5 TB/s, and one more launch), if that is under 0.8 of one part's: with 1.7
+// tiles per pair (T = 8192, D = 1024) parts measured 608 us and one part 573 to
+// 618, the power cap and not the turns setting the time.
+int dh_parts(int64_t T, int64_t D, int64_t V) {
+  constexpr int kPairs = 74;
+  const double tiles = static_cast<double>(tiles_of(T, 2 * kBM)) * tiles_of(D, kBN);
+  const int kb = tiles_of(V, kBK);
+  int best = 1;
+  double least = 0.0, one = 0.0;
+  for (int p = 1; p <= kPairs && p <= kb; ++p) {
+    const double turns = static_cast<double>(static_cast<int64_t>((tiles * p + kPairs - 1) / kPairs));
+    double us = turns * tiles_of(kb, p) * 0.3;
+    if (p > 1) us += static_cast<double>(p) * T * D * 8.0 / 5.0e6 + 3.0;
+    if (p == 1) one = least = us;
+    if (us < least && us < 0.8 * one) {
+      best = p;
+      least = us;
+    }
+  }
+  return best;
+}
+
+void set_copy(CopyArgs& a, const void* src, __half* dst, int64_t rows, int64_t D, const HeadEntries* scaled,
+              unsigned int* maxbits, float* inv) {
   a.src = static_cast<const uint4*>(src);
   a.dst = reinterpret_cast<uint4*>(dst);
   a.n_vec = rows * D / 8;
@@ -646,21 +761,22 @@ cudaError_t run_copy(const void* src, __half* dst, int64_t rows, int64_t D, cons
   }
   a.maxbits = maxbits;
   a.inv = inv;
-  const int64_t want = (a.n_vec + 1023) / 1024, cap = 8 * static_cast<int64_t>(num_sms());
-  const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
-  head_copy_kernel<<<grid, 256, 0, st>>>(a);
-  head_rescale_kernel<<<grid, 256, 0, st>>>(a);
-  note_launches(2);
-  return cudaGetLastError();
+}
+
+dim3 copy_grid(const CopyJobs& j) {
+  const int64_t n = j.w.n_vec > j.h.n_vec ? j.w.n_vec : j.h.n_vec;
+  const int64_t want = (n + 1023) / 1024, cap = 8 * static_cast<int64_t>(head_num_sms());
+  return dim3(static_cast<unsigned>(want < cap ? want : cap), 2);
 }
 
 // Backward workspace: [G' chunk: T x round_up(Vc, 64) f16][dh partial sums:
-// T x D f32, only with more than one chunk][h in fp16][the chunk's W rows in
-// fp16][copy scales].
+// T x D f32, only with more than one chunk][parts of dh: T x D f32 each][h in
+// fp16][the chunk's W rows in fp16][copy scales].
 struct BwdWs {
   int64_t ldg;
-  size_t g, acc, h16, w16, aux;
-  size_t total() const { return g + acc + h16 + w16 + aux; }
+  int parts;
+  size_t g, acc, part, h16, w16, aux;
+  size_t total() const { return g + acc + part + h16 + w16 + aux; }
 };
 
 BwdWs bwd_layout(const HeadProblem& p, int64_t Vc) {
@@ -668,6 +784,8 @@ BwdWs bwd_layout(const HeadProblem& p, int64_t Vc) {
   w.ldg = (Vc + 63) / 64 * 64;
   w.g = head_align(static_cast<size_t>(p.T) * w.ldg * 2);
   w.acc = Vc < p.V ? head_align(static_cast<size_t>(p.T) * p.D * 4) : 0;
+  w.parts = dh_parts(p.T, p.D, p.V);
+  w.part = w.parts > 1 ? head_align(static_cast<size_t>(w.parts) * p.T * p.D * 4) : 0;
   w.h16 = head_align(static_cast<size_t>(p.T) * p.D * 2);
   w.w16 = head_align(static_cast<size_t>(Vc) * p.D * 2);
   w.aux = 256;
@@ -678,8 +796,8 @@ BwdWs bwd_layout(const HeadProblem& p, int64_t Vc) {
 
 cudaError_t head_tc_forward(const HeadProblem& p, const HeadForward& f, cudaStream_t st) {
   TileMaps maps;
-  if (!make_map(&maps.a, f.h, p.D, f.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
-  if (!make_map(&maps.b, p.W, p.D, p.V, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
+  if (!head_make_map(&maps.a, f.h, p.D, f.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
+  if (!head_make_map(&maps.b, p.W, p.D, p.V, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
   TileArgs a{};
   a.rows = static_cast<int>(f.T);
   a.cols = static_cast<int>(p.V);
@@ -693,7 +811,8 @@ cudaError_t head_tc_forward(const HeadProblem& p, const HeadForward& f, cudaStre
   a.Ntot = f.en.Ntot;
   a.picked = f.picked;
   a.status = p.status;
-  return f.logits != nullptr ? run_tiles<kLogits, false>(maps, a, p.D, st) : run_tiles<kStats, false>(maps, a, p.D, st);
+  return f.logits != nullptr ? run_tiles<kLogits, false>(maps, a, p.D, 1, st)
+                             : run_tiles<kStats, false>(maps, a, p.D, 1, st);
 }
 
 size_t head_tc_bwd_bytes(const HeadProblem& p, int64_t Vc) { return bwd_layout(p, Vc).total(); }
@@ -721,6 +840,8 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
   q += w.g;
   float* acc = w.acc != 0 ? reinterpret_cast<float*>(q) : nullptr;
   q += w.acc;
+  float* part = reinterpret_cast<float*>(q);
+  q += w.part;
   __half* h16 = reinterpret_cast<__half*>(q);
   q += w.h16;
   __half* w16 = reinterpret_cast<__half*>(q);
@@ -728,20 +849,32 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
   unsigned int* maxbits = reinterpret_cast<unsigned int*>(q);          // [0] W, [1] h
   float* inv = reinterpret_cast<float*>(q + 64);
   cudaError_t err = cudaSuccess;
-  if (dW != nullptr) {
-    err = run_copy(p.h, h16, p.T, p.D, &en, maxbits + 1, inv + 1, st);
-    if (err != cudaSuccess) return err;
-  }
+  // From 2048 tokens on the tensor pipe bounds the G' kernel and two more warps of it make the fp16 copies
+  // unnoticed (they move 0.6 TB/s; a kernel of their own before it cost 48 us at V = 49152, D = 1024, of 2.9 ms);
+  // below, reading W bounds it and the copies would prolong it.
+  const bool beside = p.T >= 2048;
   for (int64_t v0 = 0; v0 < p.V; v0 += Vc) {
     const int64_t n = v0 + Vc <= p.V ? Vc : p.V - v0;
     const bool first = v0 == 0, last = v0 + n >= p.V;
     const void* Wc = static_cast<const __nv_bfloat16*>(p.W) + v0 * p.D;
+    CopyJobs copy{};
+    if (dh != nullptr) set_copy(copy.w, Wc, w16, n, p.D, nullptr, maxbits, inv);
+    if (dW != nullptr && first) set_copy(copy.h, p.h, h16, p.T, p.D, &en, maxbits + 1, inv + 1);
+    const bool any = copy.w.n_vec > 0 || copy.h.n_vec > 0;
+    if (any) {
+      err = cudaMemsetAsync(maxbits, 0, (first ? 2 : 1) * sizeof(unsigned int), st);
+      if (err != cudaSuccess) return err;
+    }
+    if (any && !beside) {
+      head_copy_kernel<<<copy_grid(copy), 256, 0, st>>>(copy);
+      note_launches(1);
+    }
     TileMaps maps;
     TileArgs a{};
     a.status = p.status;
     // G' of the chunk
-    if (!make_map(&maps.a, p.h, p.D, p.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
-    if (!make_map(&maps.b, Wc, p.D, n, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
+    if (!head_make_map(&maps.a, p.h, p.D, p.T, p.D, kBK, kBM, false)) return cudaErrorInvalidValue;
+    if (!head_make_map(&maps.b, Wc, p.D, n, p.D, kBK, kBN / 2, false)) return cudaErrorInvalidValue;
     a.rows = static_cast<int>(p.T);
     a.cols = static_cast<int>(n);
     a.v0 = static_cast<int>(v0);
@@ -753,27 +886,47 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     a.G = G;
     a.ld = w.ldg;
     a.gcols = static_cast<int>((n + 63) / 64 * 64);
-    err = run_tiles<kGrad, false>(maps, a, p.D, st);
+    if (beside) a.copy = copy;
+    err = run_tiles<kGrad, false>(maps, a, p.D, 1, st);
     if (err != cudaSuccess) return err;
+    if (any) {
+      head_rescale_kernel<<<copy_grid(copy), 256, 0, st>>>(copy);
+      note_launches(1);
+    }
     if (dh != nullptr) {
-      err = run_copy(Wc, w16, n, p.D, nullptr, maxbits, inv, st);
-      if (err != cudaSuccess) return err;
       TileArgs d{};
       d.status = p.status;
       d.rows = static_cast<int>(p.T);
       d.cols = static_cast<int>(p.D);
       d.inv = inv;
       d.row = en.row;
-      if (!make_map(&maps.a, G, a.gcols, p.T, w.ldg, kBK, kBM, true)) return cudaErrorInvalidValue;
-      if (!make_map(&maps.b, w16, p.D, n, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
-      if (last) {
+      if (!head_make_map(&maps.a, G, a.gcols, p.T, w.ldg, kBK, kBM, true)) return cudaErrorInvalidValue;
+      if (!head_make_map(&maps.b, w16, p.D, n, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (w.parts > 1) {
+        d.out = part;
+        err = run_tiles<kDh, false>(maps, d, n, w.parts, st);
+        if (err != cudaSuccess) return err;
+        ReduceArgs r{};
+        r.part = reinterpret_cast<const float4*>(part);
+        const int kb = tiles_of(n, kBK);
+        r.parts = tiles_of(kb, tiles_of(kb, w.parts));
+        r.n = p.T * p.D / 4;
+        r.vec_per_row = static_cast<int>(p.D / 4);
+        r.acc = reinterpret_cast<float4*>(acc);
+        r.acc_in = first ? 0 : 1;
+        r.row = en.row;
+        r.out = last ? static_cast<uint2*>(dh) : nullptr;
+        head_reduce_kernel<<<static_cast<unsigned>((r.n + 255) / 256), 256, 0, st>>>(r);
+        note_launches(1);
+        err = cudaGetLastError();
+      } else if (last) {
         d.out = dh;
         d.acc = first ? nullptr : acc;
-        err = run_tiles<kDh, true>(maps, d, n, st);
+        err = run_tiles<kDh, true>(maps, d, n, 1, st);
       } else {
         d.out = acc;
         d.accumulate = first ? 0 : 1;
-        err = run_tiles<kDh, false>(maps, d, n, st);
+        err = run_tiles<kDh, false>(maps, d, n, 1, st);
       }
       if (err != cudaSuccess) return err;
     }
@@ -785,14 +938,14 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
       d.inv = inv + 1;
       d.smax = en.smax;
       d.accumulate = accumulate;
-      if (!make_map(&maps.a, G, a.gcols, p.T, w.ldg, 64, kBK, true)) return cudaErrorInvalidValue;
-      if (!make_map(&maps.b, h16, p.D, p.T, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (!head_make_map(&maps.a, G, a.gcols, p.T, w.ldg, 64, kBK, true)) return cudaErrorInvalidValue;
+      if (!head_make_map(&maps.b, h16, p.D, p.T, p.D, 64, kBK, true)) return cudaErrorInvalidValue;
       if (dW_bf16) {
         d.out = static_cast<__nv_bfloat16*>(dW) + v0 * p.D;
-        err = run_tiles<kDw, true>(maps, d, p.T, st);
+        err = run_tiles<kDw, true>(maps, d, p.T, 1, st);
       } else {
         d.out = static_cast<float*>(dW) + v0 * p.D;
-        err = run_tiles<kDw, false>(maps, d, p.T, st);
+        err = run_tiles<kDw, false>(maps, d, p.T, 1, st);
       }
       if (err != cudaSuccess) return err;
     }
