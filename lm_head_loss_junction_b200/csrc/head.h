@@ -27,9 +27,11 @@ constexpr int kTopMore = 8;          // candidates beyond K that are ranked agai
 inline int64_t head_splits(int64_t V) { return (V + kHeadSplit - 1) / kHeadSplit; }
 inline size_t head_align(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Partial softmax statistics of one token over one split: the largest logit m,
-// z = sum e^(l - m) and u = sum (l - m) e^(l - m).
-typedef float4 HeadPart;             // (m, z, u, unused)
+// Partial softmax statistics of one token over one split, to base 2 (an
+// exponential is then one fma and one instruction, and l log2(e) - m is rounded
+// once): with a_v = l_v log2(e) - m for a reference m near the largest one,
+// (m, z = sum 2^a, u = sum a 2^a, the largest logit itself).
+typedef float4 HeadPart;
 
 struct HeadProblem {
   bool bf16;

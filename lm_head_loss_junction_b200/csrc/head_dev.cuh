@@ -1,0 +1,20 @@
+// Device helpers shared by the single-exit operators' kernels.
+#pragma once
+#include "common.cuh"
+
+namespace mls {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x, to about 2 units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// l log2(e) - m, rounded once.
+__device__ __forceinline__ float to_base2(float l, float m) { return fmaf(l, kLog2e, -m); }
+
+}  // namespace mls

@@ -16,6 +16,7 @@
 #include <cuda.h>
 
 #include "head.h"
+#include "head_dev.cuh"
 #include "head_host.h"
 #include "umma.cuh"
 
@@ -28,7 +29,6 @@ constexpr int kBK = 64;
 constexpr int kUK = 16;
 constexpr int kThreads = 192;            // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
 constexpr int kEpi = 128;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct FewMaps {
   CUtensorMap w, h;
@@ -198,17 +198,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
       {
         const int t = e / kSub, sub = e % kSub;
         const int n = a.V - tile * kRows;                 // rows of the tile that exist
-        float m = -INFINITY, z = 0.f, u = 0.f;
+        float top = -INFINITY, z = 0.f, u = 0.f;
         if (t < a.T) {
           for (int i = sub; i < kRows; i += kSub)
-            if (i < n) m = fmaxf(m, s.stage[t][i]);
+            if (i < n) top = fmaxf(top, s.stage[t][i]);
         }
 #pragma unroll
-        for (int o = kSub / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = kSub / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m = top * kLog2e;
         if (t < a.T) {
           for (int i = sub; i < kRows; i += kSub)
             if (i < n) {
-              const float d = s.stage[t][i] - m, x = exp2f(d * kLog2e);
+              const float d = to_base2(s.stage[t][i], m), x = ex2(d);
               z += x;
               u = fmaf(d, x, u);
             }
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
           z += __shfl_xor_sync(0xffffffffu, z, o);
           u += __shfl_xor_sync(0xffffffffu, u, o);
         }
-        if (t < a.T && sub == 0) a.part[static_cast<int64_t>(t) * a.n_tiles + tile] = make_float4(m, z, u, 0.f);
+        if (t < a.T && sub == 0) a.part[static_cast<int64_t>(t) * a.n_tiles + tile] = make_float4(m, z, u, top);
       }
       epi_sync();
     }

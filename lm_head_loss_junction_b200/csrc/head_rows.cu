@@ -2,14 +2,13 @@
 // merge of the partial statistics, and the top alternatives.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
 #include "head.h"
+#include "head_dev.cuh"
 
 namespace mls {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------ entry lists
@@ -164,12 +163,12 @@ __device__ __forceinline__ void merge_part(float& m, float& z, float& u, float m
   const float top = fmaxf(m, m2);
   if (!(top > -INFINITY)) return;                        // nothing on either side (or NaN below)
   if (z > 0.f || z != z) {
-    const float d = m - top, f = exp2f(d * kLog2e);
+    const float d = m - top, f = ex2(d);
     u = f * fmaf(d, z, u);
     z *= f;
   }
   if (z2 > 0.f || z2 != z2) {
-    const float d = m2 - top, f = exp2f(d * kLog2e);
+    const float d = m2 - top, f = ex2(d);
     u = fmaf(f, fmaf(d, z2, u2), u);
     z = fmaf(f, z2, z);
   }
@@ -197,21 +196,26 @@ __device__ __forceinline__ float entry_logit(const HeadFinish& f, int64_t t, int
   return f.picked != nullptr ? f.picked[t * tot + j] : f.logits[t * f.ld + id];
 }
 
+// A 64-bit logit likewise.
+__device__ __forceinline__ float fine_base2(double l, float m) {
+  return static_cast<float>(fma(l, 1.4426950408889634, -static_cast<double>(m)));
+}
+
 // The token's outputs that need only the statistics, by one warp.  A log
-// probability is (l - m) - log z: both are small where it is, lse is not.
-// fine: logits of the given tokens in 64 bits, or NULL.
+// probability is ln 2 ((l log2(e) - m) - log2 z): both are small where it is,
+// lse is not.  fine: logits of the given tokens in 64 bits, or NULL.
 __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int lane, float m, float logz, float mean,
                                              const double* fine) {
-  if (lane == 0) f.stats[t] = m + logz;
+  if (lane == 0) f.stats[t] = kLn2 * (m + logz);
   bool bad = false;
   if (f.y == nullptr) {
-    if (lane == 0) f.stats[f.ldT + t] = logz - mean;
+    if (lane == 0) f.stats[f.ldT + t] = kLn2 * (logz - mean);
     for (int j = lane; j < f.N; j += 32) {
       const int id = f.ids[t * f.N + j];
       const bool there = id >= 0 && id < f.V;
       float d = 0.f;
-      if (there) d = fine != nullptr ? static_cast<float>(fine[j] - m) : entry_logit(f, t, f.N, j, id) - m;
-      f.logp[t * f.N + j] = there ? d - logz : 0.f;
+      if (there) d = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, f.N, j, id), m);
+      f.logp[t * f.N + j] = there ? kLn2 * (d - logz) : 0.f;
       bad |= !there && id != -1;
     }
   } else {
@@ -236,13 +240,13 @@ __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int
         if (id < 0 || id >= f.V) continue;
         const float p = expf(f.teacher[t * f.N + j] - top);
         sum += p;
-        if (p != 0.f) kd = fmaf(p, logz - (entry_logit(f, t, tot, j, id) - m), kd);
+        if (p != 0.f) kd = fmaf(p, logz - to_base2(entry_logit(f, t, tot, j, id), m), kd);
       }
     sum = warp_sum(sum);
     kd = warp_sum(kd);
-    kd = some && !out ? kd / sum : 0.f;
+    kd = some && !out ? kLn2 * (kd / sum) : 0.f;
     if (lane == 0) {
-      const float ce = out ? 0.f : logz - (entry_logit(f, t, tot, f.N, y) - m);
+      const float ce = out ? 0.f : kLn2 * (logz - to_base2(entry_logit(f, t, tot, f.N, y), m));
       f.stats[f.ldT + t] = ce;
       f.stats[2 * f.ldT + t] = kd;
       const bool counts = !out && w != 0.f;  // 0 times a term that is not a number is not 0
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
-  finish_token(f, t, lane, m, logf(z), u / z, nullptr);
+  finish_token(f, t, lane, m, log2f(z), u / z, nullptr);
 }
 
 // ------------------------------------------------------------------ top alternatives
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   float m = -INFINITY, z = 0.f, u = 0.f;
   for (int i = threadIdx.x; i < n_splits; i += kTopThreads) {
     const HeadPart p = __ldg(f.part + t * n_splits + i);
-    keys[i] = top_key(p.x, static_cast<uint32_t>(i));
+    keys[i] = top_key(p.w, static_cast<uint32_t>(i));
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
@@ -446,8 +450,12 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   if (threadIdx.x == 0) s.count = s.n_sel = 0;
   __syncthreads();
   m = -INFINITY, z = 0.f, u = 0.f;
-#pragma unroll
-  for (int i = 0; i < kTopThreads / 32; ++i) merge_part(m, z, u, s.part[i][0], s.part[i][1], s.part[i][2]);
+  if (lane < kTopThreads / 32) {
+    m = s.part[lane][0];
+    z = s.part[lane][1];
+    u = s.part[lane][2];
+  }
+  warp_merge(m, z, u);
 
   // the splits that hold the candidates, and a lower bound on the C-th largest logit
   const int n_take = n_splits < C ? n_splits : C;
@@ -521,9 +529,9 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
       const uint64_t other = order(s.fine[i]);
       rank += other > mine || (other == mine && static_cast<uint32_t>(s.id[i]) < id);
     }
-    const float was = unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)) - m;
-    const float is = static_cast<float>(s.fine[threadIdx.x] - m);
-    const float e0 = exp2f(was * kLog2e), e1 = exp2f(is * kLog2e);
+    const float was = to_base2(unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)), m);
+    const float is = fine_base2(s.fine[threadIdx.x], m);
+    const float e0 = ex2(was), e1 = ex2(is);
     s.dz[rank] = e1 - e0;
     s.du[rank] = is * e1 - was * e0;
   }
@@ -536,11 +544,11 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   dz = warp_sum(dz);
   du = warp_sum(du);
   z += dz;
-  const float logz = logf(z);
+  const float logz = log2f(z);
   if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.fine + have);
   if (rank < f.K) {
     f.top_ids[t * f.K + rank] = static_cast<int32_t>(id);
-    f.top_logp[t * f.K + rank] = static_cast<float>(s.fine[threadIdx.x] - m) - logz;
+    f.top_logp[t * f.K + rank] = kLn2 * (fine_base2(s.fine[threadIdx.x], m) - logz);
   }
   if (threadIdx.x >= have && threadIdx.x < f.K) {
     f.top_ids[t * f.K + threadIdx.x] = -1;

@@ -2,14 +2,13 @@
 // (tensor cores would round fp32 inputs), logits of a block of tokens in the
 // workspace, any sizes.  For the small single-precision suite; bound by
 // latency there (a handful of 64 x 64 tiles).
-#include "common.cuh"
 #include "head.h"
+#include "head_dev.cuh"
 
 namespace mls {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 64, kK = 16, kThreads = 256;
 
 // C[m][n] = sum_k A(m, k) B(n, k) (+ C).  A_K / B_K: k is the operand's
@@ -107,24 +106,25 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* __restric
   if (i >= T * n_splits) return;
   const int64_t t = i / n_splits;
   const int c0 = static_cast<int>(i % n_splits) * kHeadSplit;
-  float l[4], m = -INFINITY, z = 0.f, u = 0.f;
+  float l[4], top = -INFINITY, z = 0.f, u = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int col = c0 + k * 32 + lane;
     l[k] = col < V ? logits[t * ld + col] : -INFINITY;
-    m = fmaxf(m, l[k]);
+    top = fmaxf(top, l[k]);
   }
-  m = warp_max(m);
+  top = warp_max(top);
+  const float m = top * kLog2e;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (c0 + k * 32 + lane >= V) continue;
-    const float d = l[k] - m, e = exp2f(d * kLog2e);
+    const float d = to_base2(l[k], m), e = ex2(d);
     z += e;
     u = fmaf(d, e, u);
   }
   z = warp_sum(z);
   u = warp_sum(u);
-  if (lane == 0) part[i] = make_float4(m, z, u, 0.f);
+  if (lane == 0) part[i] = make_float4(m, z, u, top);
 }
 
 // Logits -> s (q (A + B (l - lse)) + entries) in place, one block per token.
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(float* __restrict__ logi
   float* row = logits + static_cast<int64_t>(blockIdx.x) * ld;
   const float4 ri = en.row[t];
   for (int v = threadIdx.x; v < V; v += 256) {
-    const float d = row[v] - ri.x;
-    row[v] = ri.w == 0.f ? 0.f : ri.w * (exp2f(d * kLog2e) * fmaf(ri.z, d, ri.y));
+    const float d = to_base2(row[v], ri.x * kLog2e);
+    row[v] = ri.w == 0.f ? 0.f : ri.w * (ex2(d) * fmaf(ri.z * kLn2, d, ri.y));
   }
   __syncthreads();
   if (threadIdx.x == 0 && ri.w != 0.f) {

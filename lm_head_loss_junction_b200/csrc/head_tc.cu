@@ -27,6 +27,7 @@
 #include <mutex>
 
 #include "head.h"
+#include "head_dev.cuh"
 #include "head_host.h"
 #include "umma.cuh"
 
@@ -43,9 +44,9 @@ constexpr int kEpiWarps = 8;             // two per TMEM lane quadrant, 128 colu
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kCopyThreads = 64;         // two more warps: as many registers per thread as without them
 constexpr int kStageRow = 80;            // bytes of a staged row of 32 fp16 (padded against bank conflicts)
+constexpr int kStageWarp = 32 * 128;     // bytes of a warp's staging rows: 32 x 32 fp32, or fp16 rows
 constexpr int kGroupM = 8;               // row tiles per raster group: they share their A panels in L2
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMasked = -3.0e38f;      // logit of a column past V: finite, so that 0 * it is 0
+constexpr float kMasked = -1.0e38f;      // logit of a column past V: finite to base 2 too, so that 0 times it is 0
 
 enum Epi { kStats, kLogits, kGrad, kDh, kDw };
 
@@ -178,7 +179,7 @@ struct Unit {
 struct __align__(1024) TileSmem {
   uint8_t a[kStages][kBM * kBK * 2];
   uint8_t b[kStages][(kBN / 2) * kBK * 2];
-  uint8_t stage[kEpiWarps][32 * kStageRow];
+  uint8_t stage[kEpiWarps][kStageWarp];
   uint64_t full[kStages];          // leader: both CTAs' bytes
   uint64_t empty[kStages];
   uint64_t tfull[2];
@@ -276,7 +277,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     const int split = c0 / kHeadSplit;
     EntryWalk en;
     if constexpr (EPI == kStats) en.start(a, valid, t, split);
-    float m = -INFINITY, z = 0.f, u = 0.f;
+    float top = -INFINITY, m = -INFINITY, z = 0.f, u = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float r[32];
@@ -298,35 +299,52 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
         }
       }
       mask_columns(r, a.cols - col);
-      if constexpr (EPI == kLogits) {
-        if (valid) {
-          float4* dst = reinterpret_cast<float4*>(a.logits + row * a.ld + col);
+      // four running maxima and sums: the warp's own latency, not the issue rate, is what bounds this epilogue
+      float c4[4] = {r[0], r[1], r[2], r[3]};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-        }
-      }
-      float cm = r[0];
-#pragma unroll
-      for (int k = 1; k < 32; ++k) cm = fmaxf(cm, r[k]);
-      if (cm > m) {
-        // move the sums to the new maximum: (l - m') e^(l - m') = f ((l - m) + (m - m')) e^(l - m)
+      for (int k = 4; k < 32; ++k) c4[k & 3] = fmaxf(c4[k & 3], r[k]);
+      const float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+      if (cm > top) {
+        // move the sums to the new reference: with d = m - m', a' = a + d, 2^a' = 2^d 2^a
+        const float next = cm * kLog2e;
         if (z > 0.f) {
-          const float dm = m - cm;
-          const float f = exp2f(dm * kLog2e);
-          u = f * fmaf(dm, z, u);
+          const float d = m - next, f = ex2(d);
+          u = f * fmaf(d, z, u);
           z *= f;
         }
-        m = cm;
+        top = cm;
+        m = next;
       }
+      float z4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float d = r[k] - m;
-        const float e = exp2f(d * kLog2e);
-        z += e;
-        u = fmaf(d, e, u);
+        const float d = to_base2(r[k], m);
+        const float e = ex2(d);
+        z4[k & 3] += e;
+        u4[k & 3] = fmaf(d, e, u4[k & 3]);
+      }
+      z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
+      u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
+      if constexpr (EPI == kLogits) {
+        // through the warp's staging rows (16-byte pieces permuted by row, so that both sides are free of bank
+        // conflicts): a store instruction writes 4 rows x 128 contiguous bytes
+        uint8_t* stage = s.stage[warp - 2];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) * 16)) =
+              make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        __syncwarp();
+        const int64_t row0 = row - lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+          const float4 v = *reinterpret_cast<const float4*>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          if (row0 + rr < a.rows) *reinterpret_cast<float4*>(a.logits + (row0 + rr) * a.ld + col + ch * 4) = v;
+        }
+        __syncwarp();
       }
     }
-    if (valid) a.part[row * a.n_splits + split] = make_float4(m, z, u, 0.f);
+    if (valid) a.part[row * a.n_splits + split] = make_float4(m, z, u, top);
   } else if constexpr (EPI == kGrad) {
     if (c0 >= a.gcols) {
       release();
@@ -335,6 +353,8 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     const int t = static_cast<int>(row);
     const float4 ri = valid ? __ldg(a.row + t) : make_float4(0.f, 0.f, 0.f, 0.f);   // (lse, A, B, s)
     const bool live = valid && !(ri.w == 0.f);
+    const bool all_live = __all_sync(0xffffffffu, live);
+    const float lse2 = ri.x * kLog2e, A = ri.y, B2 = ri.z * kLn2;
     EntryWalk en;
     en.start(a, live && c0 < a.cols, t, (a.v0 + c0) / kHeadSplit);
     uint8_t* stage = s.stage[warp - 2];
@@ -349,9 +369,12 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       const int left = a.cols - col;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float d = r[k] - ri.x;
-        const float g = exp2f(d * kLog2e) * fmaf(ri.z, d, ri.y);
-        r[k] = live && k < left ? g : 0.f;
+        const float d = to_base2(r[k], lse2);
+        r[k] = ex2(d) * fmaf(B2, d, A);
+      }
+      if (!all_live || left < 32) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) r[k] = live && k < left ? r[k] : 0.f;
       }
       while (__any_sync(0xffffffffu, en.cur.x - a.v0 < col + 32)) {
         const bool mine = en.cur.x - a.v0 < col + 32;
