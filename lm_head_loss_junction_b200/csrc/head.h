@@ -22,7 +22,7 @@ namespace mls {
 
 constexpr int kHeadSplit = 128;      // vocabulary columns per partial statistic
 constexpr int kMaxEntries = 64;      // given tokens, teacher tokens or alternatives per token
-constexpr int kTopMore = 8;          // candidates beyond K that are ranked again in fp64
+constexpr int kTopMore = 4;          // candidates beyond K that are ranked again in 64 bits
 
 inline int64_t head_splits(int64_t V) { return (V + kHeadSplit - 1) / kHeadSplit; }
 inline size_t head_align(size_t b) { return (b + 255) & ~size_t(255); }

@@ -1,6 +1,7 @@
 // Per-token kernels of the single-exit LM-head operators: the entry lists, the
 // merge of the partial statistics, and the top alternatives.
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "head.h"
 #include "head_dev.cuh"
@@ -273,18 +274,29 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
 }
 
 // ------------------------------------------------------------------ top alternatives
-// One block per token.  The C = min(V, K + 8) largest logits by (value
+// One block per token.  The C = min(V, K + 4) largest logits by (value
 // descending, id ascending) lie in the C splits with the largest maxima by
 // (maximum descending, split ascending): were one of them in another split,
 // each chosen split's first maximum would come before it.  So only those
 // splits' logits are read, those below the C-th largest maximum are dropped,
-// and the C-th key among the rest is found by radix selection.  The candidates
-// are then ranked by products in 64 bits (exact enough that only equal logits
-// tie), so the ids do not depend on the tile a token fell into.
+// and the C-th key among the rest is found by radix selection.
+//
+// The candidates are then ranked by their products again, so that the ids do
+// not depend on the tile a token fell into (4 more than K: a logit whose fp32
+// value misplaces it by the border is among them).  First with fp32 sums of 8
+// products, added in 64 bits: each such sum is off by at most 7 half units of
+// sum |h_i w_i|, a whole product by 7 2^-24 |h| |w| (Cauchy-Schwarz).  Where two
+// neighbours among the first K + 1 are nearer than twice that, the token's
+// candidates are multiplied once more with every product exact and added in 64
+// bits; then only equal logits tie, and the lower id comes first.
+//
 // The tensor cores' accumulation truncates, which shrinks a logit by about
 // D 1e-9 of itself (2e-6 at D = 2304); the candidates' terms of z and u, the
-// ones that weigh, are replaced by those of the 64-bit logits, and so are the
+// ones that weigh, are replaced by those of these products, and so are the
 // given tokens' logits.
+//
+// T = 4096, K = 32, D = 2304: the rows of W that candidates name (0.7 GB) and
+// the 64-bit conversions bound it, not the selection.
 __device__ __forceinline__ uint32_t ordered(float f) {
   f += 0.f;                                              // -0 ranks as 0
   const uint32_t u = __float_as_uint(f);
@@ -301,8 +313,12 @@ __device__ __forceinline__ uint64_t top_key(float v, uint32_t index) {
 
 // The k-th largest of n distinct keys (1 <= k <= n) as a lower bound: exactly k
 // keys are at or above the returned value.  All kTopThreads threads of the block call it.
-template <int kTopThreads>
-__device__ uint64_t select_kth(const uint64_t* keys, int n, int k, int* hist, int* chosen) {
+// keys: an array or a function of the index.
+template <int kTopThreads, typename Keys>
+__device__ uint64_t select_kth(const Keys& keys, int n, int k, int* hist, int* chosen) {
+  const auto key_at = [&](int i) -> uint64_t {
+    if constexpr (std::is_pointer_v<Keys>) return keys[i]; else return keys(i);
+  };
   uint64_t prefix = 0;
   int shift = 56;
   for (; shift >= 0; shift -= 8) {
@@ -310,7 +326,7 @@ __device__ uint64_t select_kth(const uint64_t* keys, int n, int k, int* hist, in
     __syncthreads();
     const uint64_t above = shift == 56 ? 0 : ~uint64_t(0) << (shift + 8);
     for (int i = threadIdx.x; i < n; i += kTopThreads) {
-      const uint64_t key = keys[i];
+      const uint64_t key = key_at(i);
       if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
     }
     __syncthreads();
@@ -393,6 +409,68 @@ __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, 
     for (int o = 16; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(kFull, acc[g], o);
 }
 
+// The same with fp32 sums of 8 products, and the squared norms of the rows.
+template <int G>
+__device__ __forceinline__ void dots_fast(const void* h, const void* W, int64_t D, const int* id, int lane,
+                                          double (&acc)[G], float (&w2)[G]) {
+  const uint4* a = static_cast<const uint4*>(h);
+  const uint4* b[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    acc[g] = 0.0;
+    w2[g] = 0.f;
+    b[g] = static_cast<const uint4*>(W) + id[g] * (D / 8);
+  }
+  const int n = static_cast<int>(D / 8);
+#pragma unroll(G == 1 ? 4 : 1)
+  for (int i = lane; i < n; i += 32) {
+    uint4 w[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) w[g] = __ldg(b[g] + i);
+    float x[8];
+    bf16x8_to_f32(__ldg(a + i), x);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float y[8], p = 0.f;
+      bf16x8_to_f32(w[g], y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        p = fmaf(x[k], y[k], p);
+        w2[g] = fmaf(y[k], y[k], w2[g]);
+      }
+      acc[g] += static_cast<double>(p);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(kFull, acc[g], o);
+    w2[g] = warp_sum(w2[g]);
+  }
+}
+
+// The fast form by the block's warps; the largest squared norm to *norm (as bits).
+template <int G>
+__device__ __forceinline__ void block_dots_fast(const void* h, const void* W, int64_t D, const int* id, int n,
+                                                double* val, unsigned int* norm, int warp, int warps, int lane) {
+  for (int i = warp * G; i < n; i += warps * G) {
+    int own[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) own[g] = id[i + g < n ? i + g : n - 1];
+    double acc[G];
+    float w2[G];
+    dots_fast<G>(h, W, D, own, lane, acc, w2);
+    if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (i + g < n) {
+          val[i + g] = acc[g];
+          atomicMax(norm, __float_as_uint(w2[g]));
+        }
+    }
+  }
+}
+
 // val[i] = h . W[id[i]] for i < n, by the block's warps.
 template <bool BF16, int G>
 __device__ __forceinline__ void block_dots(const void* h, const void* W, int64_t D, const int* id, int n, double* val,
@@ -416,6 +494,8 @@ struct TopSmem {
   int chosen[4];
   float part[32][3];
   uint32_t least[32];
+  unsigned int w2, h2;                       // squared norms, as bits
+  double sorted[kMaxEntries + kTopMore];
   int count;
   int n_sel;
   int sel[kMaxEntries + kTopMore];
@@ -426,7 +506,7 @@ struct TopSmem {
 };
 
 template <bool BF16, int kTopThreads>
-__global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C) {
+__global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C, int list) {
   extern __shared__ uint8_t raw[];
   TopSmem& s = *reinterpret_cast<TopSmem*>(raw);
   uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);
@@ -447,7 +527,10 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     s.part[warp][1] = z;
     s.part[warp][2] = u;
   }
-  if (threadIdx.x == 0) s.count = s.n_sel = 0;
+  if (threadIdx.x == 0) {
+    s.count = s.n_sel = 0;
+    s.w2 = s.h2 = 0;
+  }
   __syncthreads();
   m = -INFINITY, z = 0.f, u = 0.f;
   if (lane < kTopThreads / 32) {
@@ -479,25 +562,46 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   const float* row = f.logits + t * f.ld;
   for (int i = warp; i < n_take; i += kTopThreads / 32) {
     const int c0 = s.sel[i] * kHeadSplit;
+    float v[kHeadSplit / 32];
 #pragma unroll
     for (int k = 0; k < kHeadSplit / 32; ++k) {
       const int col = c0 + k * 32 + lane;
-      if (col >= f.V) continue;
-      const uint64_t key = top_key(__ldg(row + col), static_cast<uint32_t>(col));
-      if (static_cast<uint32_t>(key >> 32) >= least) keys[atomicAdd(&s.count, 1)] = key;
+      v[k] = col < f.V ? __ldg(row + col) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kHeadSplit / 32; ++k) {
+      const int col = c0 + k * 32 + lane;
+      if (col >= f.V || ordered(v[k]) < least) continue;
+      const int at = atomicAdd(&s.count, 1);
+      if (at < list) keys[at] = top_key(v[k], static_cast<uint32_t>(col));
     }
   }
   __syncthreads();
   const int n = s.count;
-  uint64_t last = 0;
-  if (n > C) last = select_kth<kTopThreads>(keys, n, C, s.hist, s.chosen);
   if (threadIdx.x == 0) s.n_sel = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kTopThreads)
-    if (keys[i] >= last) s.fin[atomicAdd(&s.n_sel, 1)] = keys[i];
+  if (n <= list) {
+    uint64_t last = 0;
+    if (n > C) last = select_kth<kTopThreads>(keys, n, C, s.hist, s.chosen);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kTopThreads)
+      if (keys[i] >= last) s.fin[atomicAdd(&s.n_sel, 1)] = keys[i];
+  } else {
+    // many logits tie with the bound: the same selection, the keys made from the logits on every pass
+    const auto at = [&](int i) {
+      const int col = s.sel[i / kHeadSplit] * kHeadSplit + i % kHeadSplit;
+      return col < f.V ? top_key(__ldg(row + col), static_cast<uint32_t>(col)) : 0;
+    };
+    const uint64_t last = select_kth<kTopThreads>(at, n_take * kHeadSplit, C, s.hist, s.chosen);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_take * kHeadSplit; i += kTopThreads) {
+      const uint64_t key = at(i);
+      if (key >= last) s.fin[atomicAdd(&s.n_sel, 1)] = key;
+    }
+  }
   __syncthreads();
 
-  // their logits and the given tokens' as products in 64 bits (fewer than C only where logits are not numbers)
+  constexpr int kWarps = kTopThreads / 32;
+  // their logits and the given tokens' as products (fewer than C only where logits are not numbers)
   const int have = s.n_sel < C ? s.n_sel : C;
   if (threadIdx.x < have) s.id[threadIdx.x] = static_cast<int>(~static_cast<uint32_t>(s.fin[threadIdx.x]));
   if (threadIdx.x < f.N) {
@@ -506,20 +610,34 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   }
   __syncthreads();
   {
-    constexpr int kWarps = kTopThreads / 32;
     const char* hrow = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
     const int items = have + f.N;
-    if (items <= kWarps) block_dots<BF16, 1>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
-    else if (items <= 3 * kWarps) block_dots<BF16, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
-    else block_dots<BF16, 6>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+    if constexpr (BF16) {
+      // |h|^2, for the bound on the sums' error
+      float h2 = 0.f;
+      for (int i = threadIdx.x; i < f.D / 8; i += kTopThreads) {
+        float x[8];
+        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(hrow) + i), x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h2 = fmaf(x[k], x[k], h2);
+      }
+      h2 = warp_sum(h2);
+      if (lane == 0) s.part[warp][0] = h2;
+      if (items <= kWarps) block_dots_fast<1>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+      else if (items <= 3 * kWarps) block_dots_fast<3>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+      else block_dots_fast<5>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+    } else {
+      block_dots<false, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+    }
   }
   __syncthreads();
   int rank = kMaxEntries + kTopMore;
   uint32_t id = 0;
-  if (threadIdx.x < have) {
+  const auto rank_all = [&]() {
+    if (threadIdx.x >= have) return;
     id = s.id[threadIdx.x];
     // doubles as ordered integers, so that every value (a NaN too) has one rank
-    auto order = [](double d) {
+    const auto order = [](double d) {
       const int64_t b = __double_as_longlong(d + 0.0);
       return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
     };
@@ -529,6 +647,26 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
       const uint64_t other = order(s.fine[i]);
       rank += other > mine || (other == mine && static_cast<uint32_t>(s.id[i]) < id);
     }
+  };
+  rank_all();
+  if constexpr (BF16) {
+    if (threadIdx.x < have) s.sorted[rank] = s.fine[threadIdx.x];
+    __syncthreads();
+    bool near = false;
+    if (threadIdx.x < f.K && threadIdx.x + 1 < have) {
+      float h2 = 0.f;
+      for (int i = 0; i < kWarps; ++i) h2 += s.part[i][0];
+      const float off = 8.f * 5.9604645e-8f * sqrtf(h2) * sqrtf(__uint_as_float(s.w2));   // 7 and the norms' rounding
+      near = s.sorted[threadIdx.x] - s.sorted[threadIdx.x + 1] <= 2.0 * off;
+    }
+    if (__syncthreads_or(near)) {
+      const char* hrow = static_cast<const char*>(f.h) + t * f.D * 2;
+      block_dots<true, 3>(hrow, f.W, f.D, s.id, have, s.fine, warp, kWarps, lane);
+      __syncthreads();
+      rank_all();
+    }
+  }
+  if (threadIdx.x < have) {
     const float was = to_base2(unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)), m);
     const float is = fine_base2(s.fine[threadIdx.x], m);
     const float e0 = ex2(was), e1 = ex2(is);
@@ -602,9 +740,11 @@ cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
 cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const int C = static_cast<int>(f.V < f.K + kTopMore ? f.V : f.K + kTopMore);
   const int take = f.n_splits < C ? f.n_splits : C;
-  const size_t list = static_cast<size_t>(take) * kHeadSplit;
-  const size_t n = list > static_cast<size_t>(f.n_splits) ? list : static_cast<size_t>(f.n_splits);
-  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + n * sizeof(uint64_t);
+  // room for the splits' maxima, and in their place for the candidates: usually little more than C of them
+  const int most = take * kHeadSplit;
+  int list = most < 1024 ? most : 1024;
+  if (list < f.n_splits) list = f.n_splits;
+  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t);
   // Few tokens leave SMs idle: their blocks get all the warps that help.  (T = 1, D = 2304, K = 8: 24 us with 256
   // threads.)  Many tokens share an SM: 256 threads, several blocks.
   const bool wide = f.T <= 148;
@@ -612,7 +752,7 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
                    : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 256>);
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  fn<<<static_cast<unsigned>(f.T), wide ? 1024 : 256, smem, st>>>(f, C);
+  fn<<<static_cast<unsigned>(f.T), wide ? 1024 : 256, smem, st>>>(f, C, list);
   note_launches(1);
   return cudaGetLastError();
 }

@@ -9,64 +9,86 @@ namespace mls {
 
 namespace {
 
-constexpr int kTile = 64, kK = 16, kThreads = 256;
+constexpr int kK = 16, kThreads = 256;
 
 // C[m][n] = sum_k A(m, k) B(n, k) (+ C).  A_K / B_K: k is the operand's
-// contiguous dimension (row stride lda), otherwise m / n is.  64 x 64 tiles,
-// 4 x 4 outputs per thread, the next K slice loaded into registers while the
-// current one is multiplied.  krow (with !B_K): rows k of B whose .w is 0 count
-// as zeros, whatever they hold.
-template <bool A_K, bool B_K>
+// contiguous dimension (row stride lda), otherwise m / n is.  TILE x TILE
+// outputs per block, 4 x 4 per thread; with TILE = 32 the block's four groups
+// of 64 threads take a quarter of K each and their sums are added in order.
+// The next K slice is loaded into registers while the current one is
+// multiplied.  krow (with !B_K): rows k of B whose .w is 0 count as zeros,
+// whatever they hold.
+template <bool A_K, bool B_K, int TILE>
 __global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict__ A, int64_t lda,
                                                          const float* __restrict__ B, int64_t ldb,
                                                          float* __restrict__ C, int64_t ldc, int M, int N, int K,
                                                          int accumulate, const float4* __restrict__ krow) {
-  __shared__ float sa[2][kK][kTile + 4], sb[2][kK][kTile + 4];
-  const int tid = threadIdx.x;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  float ra[4], rb[4];
+  constexpr int kPer = (TILE / 4) * (TILE / 4);          // threads of a group
+  constexpr int kGroups = kThreads / kPer;
+  constexpr int kLd = TILE * kK / kPer;                  // values of each operand per thread and slice
+  __shared__ __align__(16) float sa[kGroups][2][kK][TILE + 4], sb[kGroups][2][kK][TILE + 4];
+  const int group = threadIdx.x / kPer, tid = threadIdx.x % kPer;
+  const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
+  const int per = (K + kGroups * kK - 1) / (kGroups * kK) * kK;
+  const int k_begin = group * per, k_end = min(K, k_begin + per);
+  float ra[kLd], rb[kLd];
   auto fetch = [&](int k0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = i * kThreads + tid;
-      const int ak = A_K ? e % kK : e / kTile, am = A_K ? e / kK : e % kTile;
-      const int bk = B_K ? e % kK : e / kTile, bn = B_K ? e / kK : e % kTile;
+    for (int i = 0; i < kLd; ++i) {
+      const int e = i * kPer + tid;
+      const int ak = A_K ? e % kK : e / TILE, am = A_K ? e / kK : e % TILE;
+      const int bk = B_K ? e % kK : e / TILE, bn = B_K ? e / kK : e % TILE;
       const int64_t am_g = m0 + am, bn_g = n0 + bn;
-      ra[i] = am_g < M && k0 + ak < K ? __ldg(A + (A_K ? am_g * lda + k0 + ak : (k0 + ak) * lda + am_g)) : 0.f;
-      const bool live = bn_g < N && k0 + bk < K && (B_K || krow == nullptr || krow[k0 + bk].w != 0.f);
+      ra[i] = am_g < M && k0 + ak < k_end ? __ldg(A + (A_K ? am_g * lda + k0 + ak : (k0 + ak) * lda + am_g)) : 0.f;
+      const bool live = bn_g < N && k0 + bk < k_end && (B_K || krow == nullptr || krow[k0 + bk].w != 0.f);
       rb[i] = live ? __ldg(B + (B_K ? bn_g * ldb + k0 + bk : (k0 + bk) * ldb + bn_g)) : 0.f;
     }
   };
   auto put = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = i * kThreads + tid;
-      sa[buf][A_K ? e % kK : e / kTile][A_K ? e / kK : e % kTile] = ra[i];
-      sb[buf][B_K ? e % kK : e / kTile][B_K ? e / kK : e % kTile] = rb[i];
+    for (int i = 0; i < kLd; ++i) {
+      const int e = i * kPer + tid;
+      sa[group][buf][A_K ? e % kK : e / TILE][A_K ? e / kK : e % TILE] = ra[i];
+      sb[group][buf][B_K ? e % kK : e / TILE][B_K ? e / kK : e % TILE] = rb[i];
     }
   };
-  const int tx = tid % 16, ty = tid / 16;
+  const int tx = tid % (TILE / 4), ty = tid / (TILE / 4);
   float acc[4][4] = {};
-  fetch(0);
+  fetch(k_begin);
   put(0);
   __syncthreads();
   int buf = 0;
-  for (int k0 = 0; k0 < K; k0 += kK) {
-    const bool more = k0 + kK < K;
-    if (more) fetch(k0 + kK);
+  for (int k = 0; k < per; k += kK) {
+    const bool more = k + kK < per;
+    if (more) fetch(k_begin + k + kK);
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4]);
-      const float4 b = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
+    for (int j = 0; j < kK; ++j) {
+      const float4 a = *reinterpret_cast<const float4*>(&sa[group][buf][j][ty * 4]);
+      const float4 b = *reinterpret_cast<const float4*>(&sb[group][buf][j][tx * 4]);
       const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int l = 0; l < 4; ++l) acc[i][l] = fmaf(av[i], bv[l], acc[i][l]);
     }
     if (more) put(buf ^ 1);
     __syncthreads();
     buf ^= 1;
+  }
+  if constexpr (kGroups > 1) {
+    // the groups' sums meet in shared memory (the slices are read no more)
+    float* sums = &sa[0][0][0][0];
+    static_assert(sizeof(sa) >= (kGroups - 1) * TILE * TILE * sizeof(float), "room for the sums");
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[(group - 1) * TILE * TILE + i * kPer + tid] = acc[i / 4][i % 4];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < kGroups - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] += sums[g * TILE * TILE + i * kPer + tid];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -82,20 +104,32 @@ __global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict
   }
 }
 
-template <bool A_K, bool B_K>
-cudaError_t sgemm(const float* A, int64_t lda, const float* B, int64_t ldb, float* C, int64_t ldc, int64_t M,
-                  int64_t N, int64_t K, int accumulate, const float4* krow, cudaStream_t st) {
+template <bool A_K, bool B_K, int TILE>
+cudaError_t sgemm_tiles(const float* A, int64_t lda, const float* B, int64_t ldb, float* C, int64_t ldc, int64_t M,
+                        int64_t N, int64_t K, int accumulate, const float4* krow, cudaStream_t st) {
   // grid.y is at most 65535: longer outputs go in pieces of rows
-  const int64_t most = int64_t(65535) * kTile;
+  const int64_t most = int64_t(65535) * TILE;
   for (int64_t r = 0; r < M; r += most) {
     const int64_t rows = M - r < most ? M - r : most;
-    const dim3 grid(static_cast<unsigned>((N + kTile - 1) / kTile), static_cast<unsigned>((rows + kTile - 1) / kTile));
-    sgemm_kernel<A_K, B_K><<<grid, kThreads, 0, st>>>(A_K ? A + r * lda : A + r, lda, B, ldb, C + r * ldc, ldc,
-                                                      static_cast<int>(rows), static_cast<int>(N),
-                                                      static_cast<int>(K), accumulate, krow);
+    const dim3 grid(static_cast<unsigned>((N + TILE - 1) / TILE), static_cast<unsigned>((rows + TILE - 1) / TILE));
+    sgemm_kernel<A_K, B_K, TILE><<<grid, kThreads, 0, st>>>(A_K ? A + r * lda : A + r, lda, B, ldb, C + r * ldc, ldc,
+                                                            static_cast<int>(rows), static_cast<int>(N),
+                                                            static_cast<int>(K), accumulate, krow);
     note_launches(1);
   }
   return cudaGetLastError();
+}
+
+// 64 x 64 tiles where they give every SM one; below, 32 x 32 with K in four
+// (M = 256, N = 128, K = 512: 8 blocks took 33 us).  all: the rows of the whole
+// problem, of which M may be a piece: the sums of a row do not depend on the
+// pieces.
+template <bool A_K, bool B_K>
+cudaError_t sgemm(const float* A, int64_t lda, const float* B, int64_t ldb, float* C, int64_t ldc, int64_t M,
+                  int64_t N, int64_t K, int accumulate, const float4* krow, int64_t all, cudaStream_t st) {
+  if (((all + 63) / 64) * ((N + 63) / 64) >= 148)
+    return sgemm_tiles<A_K, B_K, 64>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
+  return sgemm_tiles<A_K, B_K, 32>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
 }
 
 // One warp per (token, split).
@@ -153,7 +187,7 @@ cudaError_t head_simt_logits(const HeadProblem& p, int64_t t0, int64_t Tb, float
                              cudaStream_t st) {
   const float* h = static_cast<const float*>(p.h) + t0 * p.D;
   cudaError_t err = sgemm<true, true>(h, p.D, static_cast<const float*>(p.W), p.D, logits, ld, Tb, p.V, p.D, 0,
-                                      nullptr, st);
+                                      nullptr, p.T, st);
   if (err != cudaSuccess || part == nullptr) return err;
   const int64_t n = head_splits(p.V);
   split_stats_kernel<<<static_cast<unsigned>((Tb * n + 7) / 8), 256, 0, st>>>(logits, ld, Tb, static_cast<int>(p.V),
@@ -174,12 +208,12 @@ cudaError_t head_simt_backward(const HeadProblem& p, const HeadEntries& en, floa
                                                                static_cast<int>(head_splits(p.V)));
     note_launches(1);
     if (dh != nullptr) {
-      err = sgemm<true, false>(logits, ld, W, p.D, dh + t0 * p.D, p.D, n, p.D, p.V, 0, nullptr, st);
+      err = sgemm<true, false>(logits, ld, W, p.D, dh + t0 * p.D, p.D, n, p.D, p.V, 0, nullptr, p.T, st);
       if (err != cudaSuccess) return err;
     }
     if (dW != nullptr) {
       err = sgemm<false, false>(logits, ld, static_cast<const float*>(p.h) + t0 * p.D, p.D, dW, p.D, p.V, p.D, n,
-                                accumulate != 0 || t0 > 0, en.row + t0, st);
+                                accumulate != 0 || t0 > 0, en.row + t0, p.V, st);
       if (err != cudaSuccess) return err;
     }
   }

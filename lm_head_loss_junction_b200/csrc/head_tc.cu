@@ -226,11 +226,17 @@ __device__ __forceinline__ void mask_columns(float (&r)[32], int left) {
   }
 }
 
-// The entries of one token inside its split, in ascending id order.
+// The entries of one token inside its split, in ascending id order, two of
+// them loaded ahead.
 struct EntryWalk {
   const int2* p;
   int n;
-  int2 cur;
+  int2 cur, nxt;
+  __device__ __forceinline__ int2 load() {
+    if (n <= 0) return make_int2(INT32_MAX, 0);
+    --n;
+    return __ldg(p++);
+  }
   __device__ __forceinline__ void start(const TileArgs& a, bool valid, int t, int split) {
     n = 0;
     if (valid) {
@@ -238,15 +244,20 @@ struct EntryWalk {
       n = a.first[static_cast<int64_t>(split + 1) * a.ld_first + t] - b;
       p = a.e + static_cast<int64_t>(t) * a.Ntot + b;
     }
-    next();
+    cur = load();
+    nxt = load();
   }
   __device__ __forceinline__ void next() {
-    cur = make_int2(INT32_MAX, 0);
-    if (n > 0) {
-      cur = __ldg(p++);
-      --n;
-    }
+    cur = nxt;
+    nxt = load();
   }
+};
+
+// What a row of a tile needs besides its accumulator, loaded before the
+// epilogue waits for the accumulator so that the loads' latency is hidden.
+struct RowAhead {
+  EntryWalk en;
+  float4 ri;                       // (lse, A, B, s)
 };
 
 // A_MN / B_MN: the operand is stored with its M / N dimension contiguous
@@ -260,7 +271,7 @@ struct Layout {
 
 template <Epi EPI, bool OUT_BF16>
 __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_t acc_col, int warp, int lane,
-                                         int64_t row, int col_tile, int half, int part, uint64_t* tempty) {
+                                         int64_t row, int col_tile, int half, int part, RowAhead& ahead, uint64_t* tempty) {
   const bool valid = row < a.rows;
   const int c0 = col_tile + half * 128;
   auto release = [&]() {
@@ -275,8 +286,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     }
     const int t = static_cast<int>(row);
     const int split = c0 / kHeadSplit;
-    EntryWalk en;
-    if constexpr (EPI == kStats) en.start(a, valid, t, split);
+    EntryWalk& en = ahead.en;
     float top = -INFINITY, m = -INFINITY, z = 0.f, u = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
@@ -350,13 +360,11 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       release();
       return;
     }
-    const int t = static_cast<int>(row);
-    const float4 ri = valid ? __ldg(a.row + t) : make_float4(0.f, 0.f, 0.f, 0.f);   // (lse, A, B, s)
+    const float4 ri = ahead.ri;
     const bool live = valid && !(ri.w == 0.f);
     const bool all_live = __all_sync(0xffffffffu, live);
     const float lse2 = ri.x * kLog2e, A = ri.y, B2 = ri.z * kLn2;
-    EntryWalk en;
-    en.start(a, live && c0 < a.cols, t, (a.v0 + c0) / kHeadSplit);
+    EntryWalk& en = ahead.en;
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
 #pragma unroll 1
@@ -583,10 +591,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
     for (int i = pair; i < a.units; i += npairs, ++iter) {
       const Unit u = unit_at(a, i);
       const uint32_t buf = iter & 1;
+      const int64_t row = static_cast<int64_t>(u.mt) * 2 * kBM + rank * kBM + q * 32 + lane;
+      RowAhead ahead;
+      if constexpr (EPI == kStats || EPI == kGrad) {
+        const int c0 = u.nt * kBN + half * 128;
+        const bool here = row < a.rows && c0 < a.cols;
+        const int t = static_cast<int>(row);
+        if constexpr (EPI == kGrad) ahead.ri = row < a.rows ? __ldg(a.row + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // a row of scale 0 has entries, of coefficient 0: its G' is 0 whatever the row holds
+        ahead.en.start(a, here, t, (a.v0 + c0) / kHeadSplit);
+      }
       if (!warp_wait(&s.tfull[buf], (iter >> 1) & 1, abort, a.status)) break;
       tc_fence_after();
-      const int64_t row = static_cast<int64_t>(u.mt) * 2 * kBM + rank * kBM + q * 32 + lane;
-      epilogue<EPI, OUT_BF16>(a, s, base + buf * kBN, warp, lane, row, u.nt * kBN, half, u.part, &s.tempty[buf]);
+      epilogue<EPI, OUT_BF16>(a, s, base + buf * kBN, warp, lane, row, u.nt * kBN, half, u.part, ahead,
+                              &s.tempty[buf]);
     }
   } else if constexpr (EPI == kGrad) {
     // ---------------------------------------------------------------- fp16 copies for dh and dw
