@@ -204,15 +204,15 @@ __device__ __forceinline__ float fine_base2(double l, float m) {
 
 // The token's outputs that need only the statistics, by one warp.  A log
 // probability is ln 2 ((l log2(e) - m) - log2 z): both are small where it is,
-// lse is not.  fine: logits of the given tokens in 64 bits, or NULL.
+// lse is not.  ids: the given tokens; fine: their logits in 64 bits, or NULL.
 __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int lane, float m, float logz, float mean,
-                                             const double* fine) {
+                                             const int* ids, const double* fine) {
   if (lane == 0) f.stats[t] = kLn2 * (m + logz);
   bool bad = false;
   if (f.y == nullptr) {
     if (lane == 0) f.stats[f.ldT + t] = kLn2 * (logz - mean);
     for (int j = lane; j < f.N; j += 32) {
-      const int id = f.ids[t * f.N + j];
+      const int id = ids[j];
       const bool there = id >= 0 && id < f.V;
       float d = 0.f;
       if (there) d = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, f.N, j, id), m);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
-  finish_token(f, t, lane, m, log2f(z), u / z, nullptr);
+  finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
 }
 
 // ------------------------------------------------------------------ top alternatives
@@ -278,8 +278,11 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
 // descending, id ascending) lie in the C splits with the largest maxima by
 // (maximum descending, split ascending): were one of them in another split,
 // each chosen split's first maximum would come before it.  So only those
-// splits' logits are read, those below the C-th largest maximum are dropped,
-// and the C-th key among the rest is found by radix selection.
+// splits' logits are read.  Which they are is decided to 1/16: the maxima are
+// counted in 256 bins below the largest, the bin of the C-th is the border, and
+// a logit past it can be dropped too.  What is left (a few more than C) is
+// ranked by counting.  Where the border is past the bins or too much is left
+// (equal logits), radix selection over the whole row takes the place of it.
 //
 // The candidates are then ranked by their products again, so that the ids do
 // not depend on the tile a token fell into (4 more than K: a logit whose fp32
@@ -295,8 +298,10 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
 // ones that weigh, are replaced by those of these products, and so are the
 // given tokens' logits.
 //
-// T = 4096, K = 32, D = 2304: the rows of W that candidates name (0.7 GB) and
-// the 64-bit conversions bound it, not the selection.
+// The selection is a chain of short dependent steps (a block takes about 8 us
+// for a token whatever the sizes), several blocks per SM hide each other's; the
+// products read the rows of W that the candidates name (T = 4096, K = 32,
+// D = 2304: 0.7 GB).
 __device__ __forceinline__ uint32_t ordered(float f) {
   f += 0.f;                                              // -0 ranks as 0
   const uint32_t u = __float_as_uint(f);
@@ -489,191 +494,215 @@ __device__ __forceinline__ void block_dots(const void* h, const void* W, int64_t
   }
 }
 
+constexpr int kBins = 256;
+
 struct TopSmem {
-  int hist[256];
+  int hist[kBins];
   int chosen[4];
   float part[32][3];
-  uint32_t least[32];
-  unsigned int w2, h2;                       // squared norms, as bits
-  double sorted[kMaxEntries + kTopMore];
-  int count;
-  int n_sel;
-  int sel[kMaxEntries + kTopMore];
-  uint64_t fin[kMaxEntries + kTopMore];
-  int id[2 * kMaxEntries + kTopMore];        // the candidates, then the given tokens
-  double fine[2 * kMaxEntries + kTopMore];   // their logits in 64 bits
-  float dz[kMaxEntries + kTopMore], du[kMaxEntries + kTopMore];   // by rank: a fixed order of summation
+  float h2;
+  unsigned int w2;                           // largest squared norm of a candidate's row, as bits
+  int count, n_sel, border;
+  int given[kMaxEntries];                    // the given tokens' ids
+  int id[2 * kMaxEntries + kTopMore];        // rows to multiply: the given tokens, then the candidates by rank
+  double fine[2 * kMaxEntries + kTopMore];   // their products
+  float tile[kMaxEntries + kTopMore];        // the candidates' fp32 logits, by rank
+  int rank[kMaxEntries + kTopMore];          // their final ranks
+  float dz[kMaxEntries + kTopMore], du[kMaxEntries + kTopMore];   // by final rank: a fixed order of summation
 };
+
+// The bin of a logit or maximum: 0 at the largest, one more per 1/16 below it.
+__device__ __forceinline__ int bin_of(float largest, float v) {
+  return min(kBins - 1, static_cast<int>((largest - v) * 16.f));
+}
 
 template <bool BF16, int kTopThreads>
 __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C, int list) {
-  extern __shared__ uint8_t raw[];
+  constexpr int kWarps = kTopThreads / 32;
+  extern __shared__ __align__(16) uint8_t raw[];
   TopSmem& s = *reinterpret_cast<TopSmem*>(raw);
-  uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);   // [list]
+  float* maxima = reinterpret_cast<float*>(keys + list);                                  // [n_splits]
+  int* sel = reinterpret_cast<int*>(maxima + f.n_splits);                                 // [n_splits]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = blockIdx.x;
   const int n_splits = f.n_splits;
 
-  // the statistics, and the splits' maxima as keys
-  float m = -INFINITY, z = 0.f, u = 0.f;
+  if (threadIdx.x < f.N) {
+    const int id = f.ids[t * f.N + threadIdx.x];
+    s.given[threadIdx.x] = id;
+    s.id[threadIdx.x] = id >= 0 && id < f.V ? id : 0;
+  }
+  for (int i = threadIdx.x; i < kBins; i += kTopThreads) s.hist[i] = 0;
+  if (threadIdx.x == 0) {
+    s.count = s.n_sel = 0;
+    s.w2 = 0;
+  }
+  // the statistics, and the largest logit
+  float m = -INFINITY, z = 0.f, u = 0.f, largest = -INFINITY;
   for (int i = threadIdx.x; i < n_splits; i += kTopThreads) {
     const HeadPart p = __ldg(f.part + t * n_splits + i);
-    keys[i] = top_key(p.w, static_cast<uint32_t>(i));
+    maxima[i] = p.w;
+    largest = fmaxf(largest, p.w);
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
+  largest = warp_max(largest);
   if (lane == 0) {
     s.part[warp][0] = m;
     s.part[warp][1] = z;
     s.part[warp][2] = u;
-  }
-  if (threadIdx.x == 0) {
-    s.count = s.n_sel = 0;
-    s.w2 = s.h2 = 0;
+    s.dz[warp] = largest;
   }
   __syncthreads();
-  m = -INFINITY, z = 0.f, u = 0.f;
-  if (lane < kTopThreads / 32) {
+  m = -INFINITY, z = 0.f, u = 0.f, largest = -INFINITY;
+  if (lane < kWarps) {
     m = s.part[lane][0];
     z = s.part[lane][1];
     u = s.part[lane][2];
+    largest = s.dz[lane];
   }
   warp_merge(m, z, u);
+  largest = warp_max(largest);
 
-  // the splits that hold the candidates, and a lower bound on the C-th largest logit
-  const int n_take = n_splits < C ? n_splits : C;
-  uint64_t bound = 0;
-  if (n_splits > C) bound = select_kth<kTopThreads>(keys, n_splits, C, s.hist, s.chosen);
-  uint32_t least = 0xffffffffu;
-  for (int i = threadIdx.x; i < n_splits; i += kTopThreads)
-    if (keys[i] >= bound) {
-      s.sel[atomicAdd(&s.n_sel, 1)] = i;
-      least = min(least, static_cast<uint32_t>(keys[i] >> 32));
-    }
-  least = __reduce_min_sync(kFull, least);
-  if (lane == 0) s.least[warp] = least;
-  __syncthreads();
-  if (n_splits > C) {
-    for (int i = 0; i < kTopThreads / 32; ++i) least = min(least, s.least[i]);
-  } else {
-    least = 0;
-  }
-  // their logits at or above it (keys is read no more: the list takes its place)
+  // the border bin of the maxima, the splits on this side of it, their logits on this side of it
+  // (with fewer splits than candidates, the border of the logits themselves)
   const float* row = f.logits + t * f.ld;
-  for (int i = warp; i < n_take; i += kTopThreads / 32) {
-    const int c0 = s.sel[i] * kHeadSplit;
-    float v[kHeadSplit / 32];
+  if (n_splits >= C) {
+    for (int i = threadIdx.x; i < n_splits; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, maxima[i])], 1);
+  } else {
+    for (int i = threadIdx.x; i < f.V; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, __ldg(row + i))], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int own[kBins / 32], sum = 0;
 #pragma unroll
-    for (int k = 0; k < kHeadSplit / 32; ++k) {
-      const int col = c0 + k * 32 + lane;
-      v[k] = col < f.V ? __ldg(row + col) : 0.f;
+    for (int i = 0; i < kBins / 32; ++i) {
+      own[i] = s.hist[lane * (kBins / 32) + i];
+      sum += own[i];
     }
+    int before = sum;
 #pragma unroll
-    for (int k = 0; k < kHeadSplit / 32; ++k) {
-      const int col = c0 + k * 32 + lane;
-      if (col >= f.V || ordered(v[k]) < least) continue;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += v;
+    }
+    before -= sum;
+    int border = kBins - 1;
+#pragma unroll
+    for (int i = kBins / 32 - 1; i >= 0; --i) {
+      sum -= own[i];
+      if (before + sum < C && C <= before + sum + own[i]) border = lane * (kBins / 32) + i;
+    }
+    border = __reduce_min_sync(kFull, border);
+    if (lane == 0) s.border = border;
+  }
+  __syncthreads();
+  const int border = s.border;
+  for (int i = threadIdx.x; i < n_splits; i += kTopThreads)
+    if (bin_of(largest, maxima[i]) <= border) sel[atomicAdd(&s.n_sel, 1)] = i;
+  __syncthreads();
+  const int n_take = s.n_sel;
+  for (int i = warp; i < n_take; i += kWarps) {
+    const int col = sel[i] * kHeadSplit + lane * 4;
+    if (col >= f.V) continue;                            // rows are padded to a multiple of 64
+    const float4 v4 = __ldg(reinterpret_cast<const float4*>(row + col));
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (col + k >= f.V || bin_of(largest, v[k]) > border) continue;
       const int at = atomicAdd(&s.count, 1);
-      if (at < list) keys[at] = top_key(v[k], static_cast<uint32_t>(col));
+      if (at < list) keys[at] = top_key(v[k], static_cast<uint32_t>(col + k));
     }
   }
   __syncthreads();
-  const int n = s.count;
-  if (threadIdx.x == 0) s.n_sel = 0;
-  if (n <= list) {
-    uint64_t last = 0;
-    if (n > C) last = select_kth<kTopThreads>(keys, n, C, s.hist, s.chosen);
+  int n = s.count;
+  if (n > list) {
+    // keys made from the logits on every pass; C of them are at or above the C-th
+    const auto at = [&](int i) { return top_key(__ldg(row + i), static_cast<uint32_t>(i)); };
+    const uint64_t last = select_kth<kTopThreads>(at, static_cast<int>(f.V), C, s.hist, s.chosen);
+    if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kTopThreads)
-      if (keys[i] >= last) s.fin[atomicAdd(&s.n_sel, 1)] = keys[i];
-  } else {
-    // many logits tie with the bound: the same selection, the keys made from the logits on every pass
-    const auto at = [&](int i) {
-      const int col = s.sel[i / kHeadSplit] * kHeadSplit + i % kHeadSplit;
-      return col < f.V ? top_key(__ldg(row + col), static_cast<uint32_t>(col)) : 0;
-    };
-    const uint64_t last = select_kth<kTopThreads>(at, n_take * kHeadSplit, C, s.hist, s.chosen);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_take * kHeadSplit; i += kTopThreads) {
+    for (int i = threadIdx.x; i < f.V; i += kTopThreads) {
       const uint64_t key = at(i);
-      if (key >= last) s.fin[atomicAdd(&s.n_sel, 1)] = key;
+      if (key >= last) keys[atomicAdd(&s.count, 1)] = key;
+    }
+    __syncthreads();
+    n = s.count;
+  }
+  const int have = n < C ? n : C;                        // fewer only where logits are not numbers
+  for (int i = threadIdx.x; i < n; i += kTopThreads) {
+    const uint64_t key = keys[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += keys[j] > key;
+    if (rank < C) {
+      s.id[f.N + rank] = static_cast<int>(~static_cast<uint32_t>(key));
+      s.tile[rank] = unordered(static_cast<uint32_t>(key >> 32));
     }
   }
   __syncthreads();
 
-  constexpr int kWarps = kTopThreads / 32;
-  // their logits and the given tokens' as products (fewer than C only where logits are not numbers)
-  const int have = s.n_sel < C ? s.n_sel : C;
-  if (threadIdx.x < have) s.id[threadIdx.x] = static_cast<int>(~static_cast<uint32_t>(s.fin[threadIdx.x]));
-  if (threadIdx.x < f.N) {
-    const int id = f.ids[t * f.N + threadIdx.x];
-    s.id[have + threadIdx.x] = id >= 0 && id < f.V ? id : 0;
-  }
-  __syncthreads();
-  {
-    const char* hrow = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
-    const int items = have + f.N;
-    if constexpr (BF16) {
+  // the given tokens' and the candidates' logits as products
+  const char* hrow = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
+  const int items = f.N + have;
+  if constexpr (BF16) {
+    if (warp == kWarps - 1) {
       // |h|^2, for the bound on the sums' error
       float h2 = 0.f;
-      for (int i = threadIdx.x; i < f.D / 8; i += kTopThreads) {
+      for (int i = lane; i < f.D / 8; i += 32) {
         float x[8];
         bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(hrow) + i), x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h2 = fmaf(x[k], x[k], h2);
       }
       h2 = warp_sum(h2);
-      if (lane == 0) s.part[warp][0] = h2;
-      if (items <= kWarps) block_dots_fast<1>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
-      else if (items <= 3 * kWarps) block_dots_fast<3>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
-      else block_dots_fast<5>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
-    } else {
-      block_dots<false, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+      if (lane == 0) s.h2 = h2;
     }
+    if (items <= kWarps) block_dots_fast<1>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+    else if (items <= 3 * kWarps) block_dots_fast<3>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+    else block_dots_fast<5>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
+  } else {
+    block_dots<false, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
   }
   __syncthreads();
-  int rank = kMaxEntries + kTopMore;
-  uint32_t id = 0;
-  const auto rank_all = [&]() {
-    if (threadIdx.x >= have) return;
-    id = s.id[threadIdx.x];
-    // doubles as ordered integers, so that every value (a NaN too) has one rank
-    const auto order = [](double d) {
-      const int64_t b = __double_as_longlong(d + 0.0);
-      return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
-    };
-    const uint64_t mine = order(s.fine[threadIdx.x]);
-    rank = 0;
-    for (int i = 0; i < have; ++i) {
-      const uint64_t other = order(s.fine[i]);
-      rank += other > mine || (other == mine && static_cast<uint32_t>(s.id[i]) < id);
-    }
-  };
-  rank_all();
-  if constexpr (BF16) {
-    if (threadIdx.x < have) s.sorted[rank] = s.fine[threadIdx.x];
+  // still in that order, no two of the first K + 1 nearer than the error, none of the rest among the first K?
+  const int r = threadIdx.x;
+  const double* fine = s.fine + f.N;
+  bool keep = true;
+  if ((r + 1 < have && r < f.K) || (r > f.K && r < have)) {
+    double off = 0.0;                                    // fp32 inputs: these products are the exact ones
+    if constexpr (BF16) off = 2.f * 8.f * 5.9604645e-8f * sqrtf(s.h2) * sqrtf(__uint_as_float(s.w2));   // 7, and the norms' rounding
+    keep = (r < f.K ? fine[r] - fine[r + 1] : fine[f.K - 1] - fine[r]) > off;
+  }
+  if (r < have) s.rank[r] = r;
+  if (__syncthreads_or(!keep)) {
+    if constexpr (BF16) block_dots<true, 3>(hrow, f.W, f.D, s.id + f.N, have, s.fine + f.N, warp, kWarps, lane);
     __syncthreads();
-    bool near = false;
-    if (threadIdx.x < f.K && threadIdx.x + 1 < have) {
-      float h2 = 0.f;
-      for (int i = 0; i < kWarps; ++i) h2 += s.part[i][0];
-      const float off = 8.f * 5.9604645e-8f * sqrtf(h2) * sqrtf(__uint_as_float(s.w2));   // 7 and the norms' rounding
-      near = s.sorted[threadIdx.x] - s.sorted[threadIdx.x + 1] <= 2.0 * off;
-    }
-    if (__syncthreads_or(near)) {
-      const char* hrow = static_cast<const char*>(f.h) + t * f.D * 2;
-      block_dots<true, 3>(hrow, f.W, f.D, s.id, have, s.fine, warp, kWarps, lane);
-      __syncthreads();
-      rank_all();
+    if (r < have) {
+      // doubles as ordered integers, so that every value (a NaN too) has one rank
+      const auto order = [](double d) {
+        const int64_t b = __double_as_longlong(d + 0.0);
+        return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
+      };
+      const uint64_t mine = order(fine[r]);
+      int rank = 0;
+      for (int i = 0; i < have; ++i) {
+        const uint64_t other = order(fine[i]);
+        rank += other > mine || (other == mine && s.id[f.N + i] < s.id[f.N + r]);
+      }
+      s.rank[r] = rank;
     }
   }
-  if (threadIdx.x < have) {
-    const float was = to_base2(unordered(static_cast<uint32_t>(s.fin[threadIdx.x] >> 32)), m);
-    const float is = fine_base2(s.fine[threadIdx.x], m);
+  const int rank = r < have ? s.rank[r] : 0;
+  if (r < have) {
+    const float was = to_base2(s.tile[r], m), is = fine_base2(fine[r], m);
     const float e0 = ex2(was), e1 = ex2(is);
     s.dz[rank] = e1 - e0;
     s.du[rank] = is * e1 - was * e0;
   }
   __syncthreads();
+  if (warp * 32 >= kMaxEntries + kTopMore) return;
   float dz = 0.f, du = 0.f;
   for (int i = lane; i < have; i += 32) {
     dz += s.dz[i];
@@ -683,14 +712,14 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   du = warp_sum(du);
   z += dz;
   const float logz = log2f(z);
-  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.fine + have);
-  if (rank < f.K) {
-    f.top_ids[t * f.K + rank] = static_cast<int32_t>(id);
-    f.top_logp[t * f.K + rank] = kLn2 * (fine_base2(s.fine[threadIdx.x], m) - logz);
+  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.given, s.fine);
+  if (r < have && rank < f.K) {
+    f.top_ids[t * f.K + rank] = s.id[f.N + r];
+    f.top_logp[t * f.K + rank] = kLn2 * (fine_base2(fine[r], m) - logz);
   }
-  if (threadIdx.x >= have && threadIdx.x < f.K) {
-    f.top_ids[t * f.K + threadIdx.x] = -1;
-    f.top_logp[t * f.K + threadIdx.x] = NAN;
+  if (r >= have && r < f.K) {
+    f.top_ids[t * f.K + r] = -1;
+    f.top_logp[t * f.K + r] = NAN;
   }
 }
 
@@ -739,14 +768,13 @@ cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
 
 cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const int C = static_cast<int>(f.V < f.K + kTopMore ? f.V : f.K + kTopMore);
-  const int take = f.n_splits < C ? f.n_splits : C;
-  // room for the splits' maxima, and in their place for the candidates: usually little more than C of them
-  const int most = take * kHeadSplit;
-  int list = most < 1024 ? most : 1024;
-  if (list < f.n_splits) list = f.n_splits;
-  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t);
+  // room for what the selection leaves: usually little more than C; the whole of a short row; never less than C
+  const int64_t padded = (f.V + 1) / 2 * 2;
+  const int list = padded < 1024 ? static_cast<int>(padded) : 1024;
+  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t) +
+                      static_cast<size_t>(f.n_splits) * 8;
   // Few tokens leave SMs idle: their blocks get all the warps that help.  (T = 1, D = 2304, K = 8: 24 us with 256
-  // threads.)  Many tokens share an SM: 256 threads, several blocks.
+  // threads, 15 with 1024.)  Many tokens share an SM: 256 threads, several blocks.
   const bool wide = f.T <= 148;
   auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : head_top_kernel<true, 256>)
                    : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 256>);
