@@ -64,7 +64,8 @@ struct HeadEntries {
   int2* e;                         // [T][Ntot] (id, position or coefficient bits)
   uint8_t* first;                  // [splits + 1][T]
   float4* row;                     // [T] (lse, A, B, s); backward only
-  unsigned int* smax;              // largest s as float bits; backward only
+  unsigned int* smax;              // backward only: largest s as float bits, [1] and [2] the largest magnitudes of
+                                   // the fp16 copies of W and h (all three set to 0 with the entries)
   int Ntot;
 };
 size_t head_entries_bytes(int64_t T, int64_t V, int Ntot, bool backward);

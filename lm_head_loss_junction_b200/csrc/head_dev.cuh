@@ -17,4 +17,12 @@ __device__ __forceinline__ float ex2(float x) {
 // l log2(e) - m, rounded once.
 __device__ __forceinline__ float to_base2(float l, float m) { return fmaf(l, kLog2e, -m); }
 
+// The kernels of one call are launched so that the next may be set up while one
+// runs; each thread waits here, before its first access to global memory, until
+// everything before on the stream is complete and visible.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 }  // namespace mls

@@ -95,6 +95,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
     tmem_alloc(&s.tmem_base, F::kCols);
     tmem_relinquish();
   }
+  // The thread that made the barriers is the one that loads: its first loads are on their way before the other warps
+  // are set up.  (block g of the first tile is kb = g: a tile shorter than the ring starts with its own blocks only)
+  after_previous();
+  const int early = static_cast<int>(blockIdx.x) < a.n_tiles ? (a.kblocks < kStages ? a.kblocks : kStages) : 0;
+  if (threadIdx.x == 0) {
+    for (int kb = 0; kb < early; ++kb) {
+      mbar_arrive_expect_tx(&s.full[kb], F::kStageBytes);
+      tma_load_2d(&maps.w, &s.full[kb], s.w[kb], kb * kBK, static_cast<int>(blockIdx.x) * kRows);
+      tma_load_2d(&maps.h, &s.full[kb], s.h[kb], kb * kBK, 0);
+    }
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -104,10 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, issued = 0;
+      uint32_t stage = early % kStages, phase = early / kStages, issued = early;
       bool ok = true;
       for (int tile = blockIdx.x; tile < a.n_tiles && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < a.kblocks; ++kb) {
+        for (int kb = tile == static_cast<int>(blockIdx.x) ? early : 0; kb < a.kblocks; ++kb) {
           if (!mbar_wait(&s.empty[stage], phase ^ 1, abort, a.status)) { ok = false; break; }
           mbar_arrive_expect_tx(&s.full[stage], F::kStageBytes);
           tma_load_2d(&maps.w, &s.full[stage], s.w[stage], kb * kBK, tile * kRows);
@@ -198,21 +210,36 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
       {
         const int t = e / kSub, sub = e % kSub;
         const int n = a.V - tile * kRows;                 // rows of the tile that exist
-        float top = -INFINITY, z = 0.f, u = 0.f;
-        if (t < a.T) {
-          for (int i = sub; i < kRows; i += kSub)
-            if (i < n) top = fmaxf(top, s.stage[t][i]);
-        }
+        // at most 32 values of the token in registers at a time, so that their loads do not wait for one another
+        constexpr int kOwn = kRows / kSub, kChunk = kOwn < 32 ? kOwn : 32;
+        float top = -INFINITY, m = -INFINITY, z = 0.f, u = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < kOwn; c += kChunk) {
+          float l[kChunk], cm = -INFINITY;
 #pragma unroll
-        for (int o = kSub / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float m = top * kLog2e;
-        if (t < a.T) {
-          for (int i = sub; i < kRows; i += kSub)
-            if (i < n) {
-              const float d = to_base2(s.stage[t][i], m), x = ex2(d);
-              z += x;
-              u = fmaf(d, x, u);
+          for (int k = 0; k < kChunk; ++k) {
+            const int i = (c + k) * kSub + sub;
+            l[k] = t < a.T && i < n ? s.stage[t][i] : -1.0e38f;      // finite to base 2 too: 0 times it is 0
+            cm = fmaxf(cm, l[k]);
+          }
+#pragma unroll
+          for (int o = kSub / 2; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+          if (cm > top) {
+            const float next = cm * kLog2e;
+            if (z > 0.f) {
+              const float d = m - next, f = ex2(d);
+              u = f * fmaf(d, z, u);
+              z *= f;
             }
+            top = cm;
+            m = next;
+          }
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k) {
+            const float d = to_base2(l[k], m), x = ex2(d);
+            z += x;
+            u = fmaf(d, x, u);
+          }
         }
 #pragma unroll
         for (int o = kSub / 2; o > 0; o >>= 1) {
@@ -242,9 +269,7 @@ cudaError_t run_few(const FewMaps& maps, const FewArgs& a, cudaStream_t st) {
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   const int sms = head_num_sms();
-  fn<<<a.n_tiles < sms ? a.n_tiles : sms, kThreads, smem, st>>>(maps, a);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(fn, dim3(static_cast<unsigned>(a.n_tiles < sms ? a.n_tiles : sms)), kThreads, smem, st, maps, a);
 }
 
 }  // namespace

@@ -1,7 +1,11 @@
 // Host helpers shared by the tensor-core files of the single-exit operators.
 #pragma once
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <cstdint>
+#include <utility>
+
+#include "kernels.h"
 
 namespace mls {
 
@@ -13,5 +17,26 @@ bool head_make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t ou
 
 // SMs of the current device.
 int head_num_sms();
+
+// Launches a kernel that calls after_previous() (head_dev.cuh) before it touches
+// global memory: it may be set up while the one before it on the stream ends.
+// A step of a few tokens is ten launches of a few microseconds each, of which
+// the gaps were a sixth.
+template <typename... P, typename... A>
+cudaError_t head_launch(void (*fn)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+  note_launches(1);
+  return err;
+}
 
 }  // namespace mls

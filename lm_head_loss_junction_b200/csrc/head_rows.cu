@@ -5,6 +5,7 @@
 
 #include "head.h"
 #include "head_dev.cuh"
+#include "head_host.h"
 
 namespace mls {
 
@@ -23,8 +24,10 @@ constexpr int kEntryTokens = 8;
 constexpr int kMaxTot = kMaxEntries + 1;
 constexpr int kPerLane = (kMaxTot + 31) / 32;
 
+constexpr int kPadTot = (kMaxTot + 3) / 4 * 4;
+
 struct EntrySmem {
-  int id[kEntryTokens][kMaxTot];
+  uint32_t key[kEntryTokens][kPadTot];
   int sorted[kEntryTokens][kMaxTot];
   int count[kEntryTokens];
 };
@@ -38,7 +41,8 @@ __device__ __forceinline__ float pow2_of(float m) {
 
 __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn in, const HeadEntries out,
                                                            bool backward, int n_splits, int32_t* status) {
-  __shared__ EntrySmem s;
+  __shared__ __align__(16) EntrySmem s;
+  after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kEntryTokens;
   const int N = in.N, tot = out.Ntot;
@@ -117,42 +121,63 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
       }
     }
     if (__any_sync(kFull, bad) && lane == 0) set_flag(status, MLS_DEVFLAG_BAD_ID);
+    // rank by (id, position): in one word where the id leaves room for the position, else in two steps
+    const bool packed = in.V <= (int64_t(1) << 25);
     int n = 0;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int j = k * 32 + lane;
       n += __popc(__ballot_sync(kFull, there[k]));
-      if (j < tot) s.id[i][j] = there[k] ? id[k] : INT32_MAX;
+      const uint32_t word = packed ? static_cast<uint32_t>(id[k]) << 7 | j : static_cast<uint32_t>(id[k]);
+      if (j < kPadTot) s.key[i][j] = there[k] ? word : 0xffffffffu;
     }
     if (lane == 0) s.count[i] = n;
     __syncwarp();
     const float r = scale != 0.f ? 1.f / scale : 0.f;
+    int rank[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) rank[k] = 0;
+    if (packed) {
+      for (int o = 0; o < tot; o += 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(&s.key[i][o]);
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const uint32_t mine = static_cast<uint32_t>(id[k]) << 7 | (k * 32 + lane);
+          rank[k] += (w.x < mine) + (w.y < mine) + (w.z < mine) + (w.w < mine);
+        }
+      }
+    } else {
+      for (int o = 0; o < tot; ++o) {
+        const uint32_t w = s.key[i][o];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const uint32_t mine = static_cast<uint32_t>(id[k]);
+          rank[k] += w < mine || (w == mine && o < k * 32 + lane);
+        }
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      const int j = k * 32 + lane;
       if (!there[k]) continue;
-      int rank = 0;
-#pragma unroll 8
-      for (int o = 0; o < tot; ++o) {
-        const int other = s.id[i][o];
-        rank += other < id[k] || (other == id[k] && o < j);
-      }
-      s.sorted[i][rank] = id[k];
-      out.e[t * tot + rank] = make_int2(id[k], backward ? __float_as_int(c[k] * r) : j);
+      s.sorted[i][rank[k]] = id[k];
+      out.e[t * tot + rank[k]] = make_int2(id[k], backward ? __float_as_int(c[k] * r) : k * 32 + lane);
     }
   }
   __syncthreads();
+  // each thread walks a range of splits of one token: one search, then steps
   const int own = threadIdx.x % kEntryTokens;
   const int64_t t = t0 + own;
   if (t < in.T) {
     const int n = s.count[own];
-    for (int sp = threadIdx.x / kEntryTokens; sp <= n_splits; sp += 256 / kEntryTokens) {
-      const int64_t edge = static_cast<int64_t>(sp) * kHeadSplit;
-      int lo = 0, hi = n;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s.sorted[own][mid] < edge) lo = mid + 1; else hi = mid;
-      }
+    const int per = (n_splits + 256 / kEntryTokens) / (256 / kEntryTokens);
+    const int begin = threadIdx.x / kEntryTokens * per, end = min(begin + per, n_splits + 1);
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s.sorted[own][mid] < static_cast<int64_t>(begin) * kHeadSplit) lo = mid + 1; else hi = mid;
+    }
+    for (int sp = begin; sp < end; ++sp) {
+      while (lo < n && s.sorted[own][lo] < static_cast<int64_t>(sp) * kHeadSplit) ++lo;
       out.first[static_cast<int64_t>(sp) * in.T + t] = static_cast<uint8_t>(lo);
     }
   }
@@ -261,6 +286,7 @@ __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int
 }
 
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
+  after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= f.T) return;
@@ -528,6 +554,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   const int64_t t = blockIdx.x;
   const int n_splits = f.n_splits;
 
+  after_previous();
   if (threadIdx.x < f.N) {
     const int id = f.ids[t * f.N + threadIdx.x];
     s.given[threadIdx.x] = id;
@@ -751,19 +778,16 @@ HeadEntries head_entries_layout(int64_t T, int64_t V, int Ntot, bool backward, v
 cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bool backward, int32_t* status,
                              cudaStream_t st) {
   if (backward) {
-    const cudaError_t err = cudaMemsetAsync(out.smax, 0, sizeof(unsigned int), st);
+    const cudaError_t err = cudaMemsetAsync(out.smax, 0, 3 * sizeof(unsigned int), st);
     if (err != cudaSuccess) return err;
   }
   const unsigned grid = static_cast<unsigned>((in.T + kEntryTokens - 1) / kEntryTokens);
-  head_entries_kernel<<<grid, 256, 0, st>>>(in, out, backward, static_cast<int>(head_splits(in.V)), status);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(head_entries_kernel, dim3(grid), 256, 0, st, in, out, backward,
+                     static_cast<int>(head_splits(in.V)), status);
 }
 
 cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
-  head_finish_kernel<<<static_cast<unsigned>((f.T + 7) / 8), 256, 0, st>>>(f);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(head_finish_kernel, dim3(static_cast<unsigned>((f.T + 7) / 8)), 256, 0, st, f);
 }
 
 cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
@@ -780,9 +804,7 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
                    : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 256>);
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  fn<<<static_cast<unsigned>(f.T), wide ? 1024 : 256, smem, st>>>(f, C, list);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(fn, dim3(static_cast<unsigned>(f.T)), wide ? 1024u : 256u, smem, st, f, C, list);
 }
 
 }  // namespace mls

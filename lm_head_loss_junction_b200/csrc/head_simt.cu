@@ -4,17 +4,18 @@
 // latency there (a handful of 64 x 64 tiles).
 #include "head.h"
 #include "head_dev.cuh"
+#include "head_host.h"
 
 namespace mls {
 
 namespace {
 
-constexpr int kK = 16, kThreads = 256;
+constexpr int kThreads = 256;
 
 // C[m][n] = sum_k A(m, k) B(n, k) (+ C).  A_K / B_K: k is the operand's
 // contiguous dimension (row stride lda), otherwise m / n is.  TILE x TILE
-// outputs per block, 4 x 4 per thread; with TILE = 32 the block's four groups
-// of 64 threads take a quarter of K each and their sums are added in order.
+// outputs per block, 4 x 4 per thread; with TILE = 32 (16) the block's 4 (16)
+// groups of threads take a part of K each and their sums are added in order.
 // The next K slice is loaded into registers while the current one is
 // multiplied.  krow (with !B_K): rows k of B whose .w is 0 count as zeros,
 // whatever they hold.
@@ -23,10 +24,12 @@ __global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict
                                                          const float* __restrict__ B, int64_t ldb,
                                                          float* __restrict__ C, int64_t ldc, int M, int N, int K,
                                                          int accumulate, const float4* __restrict__ krow) {
+  constexpr int kK = TILE == 16 ? 16 : 32;               // K per slice
   constexpr int kPer = (TILE / 4) * (TILE / 4);          // threads of a group
   constexpr int kGroups = kThreads / kPer;
   constexpr int kLd = TILE * kK / kPer;                  // values of each operand per thread and slice
-  __shared__ __align__(16) float sa[kGroups][2][kK][TILE + 4], sb[kGroups][2][kK][TILE + 4];
+  __shared__ __align__(16) float sa[kGroups][kK][TILE + 4], sb[kGroups][kK][TILE + 4];
+  after_previous();
   const int group = threadIdx.x / kPer, tid = threadIdx.x % kPer;
   const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
   const int per = (K + kGroups * kK - 1) / (kGroups * kK) * kK;
@@ -44,40 +47,36 @@ __global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict
       rb[i] = live ? __ldg(B + (B_K ? bn_g * ldb + k0 + bk : (k0 + bk) * ldb + bn_g)) : 0.f;
     }
   };
-  auto put = [&](int buf) {
+  auto put = [&]() {
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
       const int e = i * kPer + tid;
-      sa[group][buf][A_K ? e % kK : e / TILE][A_K ? e / kK : e % TILE] = ra[i];
-      sb[group][buf][B_K ? e % kK : e / TILE][B_K ? e / kK : e % TILE] = rb[i];
+      sa[group][A_K ? e % kK : e / TILE][A_K ? e / kK : e % TILE] = ra[i];
+      sb[group][B_K ? e % kK : e / TILE][B_K ? e / kK : e % TILE] = rb[i];
     }
   };
   const int tx = tid % (TILE / 4), ty = tid / (TILE / 4);
   float acc[4][4] = {};
   fetch(k_begin);
-  put(0);
-  __syncthreads();
-  int buf = 0;
   for (int k = 0; k < per; k += kK) {
-    const bool more = k + kK < per;
-    if (more) fetch(k_begin + k + kK);
+    put();
+    __syncthreads();
+    if (k + kK < per) fetch(k_begin + k + kK);
 #pragma unroll
     for (int j = 0; j < kK; ++j) {
-      const float4 a = *reinterpret_cast<const float4*>(&sa[group][buf][j][ty * 4]);
-      const float4 b = *reinterpret_cast<const float4*>(&sb[group][buf][j][tx * 4]);
+      const float4 a = *reinterpret_cast<const float4*>(&sa[group][j][ty * 4]);
+      const float4 b = *reinterpret_cast<const float4*>(&sb[group][j][tx * 4]);
       const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int l = 0; l < 4; ++l) acc[i][l] = fmaf(av[i], bv[l], acc[i][l]);
     }
-    if (more) put(buf ^ 1);
     __syncthreads();
-    buf ^= 1;
   }
   if constexpr (kGroups > 1) {
     // the groups' sums meet in shared memory (the slices are read no more)
-    float* sums = &sa[0][0][0][0];
+    float* sums = &sa[0][0][0];
     static_assert(sizeof(sa) >= (kGroups - 1) * TILE * TILE * sizeof(float), "room for the sums");
     if (group > 0) {
 #pragma unroll
@@ -112,16 +111,18 @@ cudaError_t sgemm_tiles(const float* A, int64_t lda, const float* B, int64_t ldb
   for (int64_t r = 0; r < M; r += most) {
     const int64_t rows = M - r < most ? M - r : most;
     const dim3 grid(static_cast<unsigned>((N + TILE - 1) / TILE), static_cast<unsigned>((rows + TILE - 1) / TILE));
-    sgemm_kernel<A_K, B_K, TILE><<<grid, kThreads, 0, st>>>(A_K ? A + r * lda : A + r, lda, B, ldb, C + r * ldc, ldc,
-                                                            static_cast<int>(rows), static_cast<int>(N),
-                                                            static_cast<int>(K), accumulate, krow);
-    note_launches(1);
+    const cudaError_t err =
+        head_launch(sgemm_kernel<A_K, B_K, TILE>, grid, kThreads, 0, st, A_K ? A + r * lda : A + r, lda, B, ldb,
+                    C + r * ldc, ldc, static_cast<int>(rows), static_cast<int>(N), static_cast<int>(K), accumulate, krow);
+    if (err != cudaSuccess) return err;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
-// 64 x 64 tiles where they give every SM one; below, 32 x 32 with K in four
-// (M = 256, N = 128, K = 512: 8 blocks took 33 us).  all: the rows of the whole
+// The largest tiles that give every SM one, or every other SM one of 32 x 32
+// (M = 256, N = 128, K = 512: 8 blocks of 64 x 64 took 33 us, 32 of 32 x 32
+// 15 us, 128 of 16 x 16 7.5 us; M = 256, N = 512, K = 192: 128 of 32 x 32 5 us,
+// 512 of 16 x 16 8.5 us).  all: the rows of the whole
 // problem, of which M may be a piece: the sums of a row do not depend on the
 // pieces.
 template <bool A_K, bool B_K>
@@ -129,12 +130,15 @@ cudaError_t sgemm(const float* A, int64_t lda, const float* B, int64_t ldb, floa
                   int64_t N, int64_t K, int accumulate, const float4* krow, int64_t all, cudaStream_t st) {
   if (((all + 63) / 64) * ((N + 63) / 64) >= 148)
     return sgemm_tiles<A_K, B_K, 64>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
-  return sgemm_tiles<A_K, B_K, 32>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
+  if (((all + 31) / 32) * ((N + 31) / 32) >= 74)
+    return sgemm_tiles<A_K, B_K, 32>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
+  return sgemm_tiles<A_K, B_K, 16>(A, lda, B, ldb, C, ldc, M, N, K, accumulate, krow, st);
 }
 
 // One warp per (token, split).
 __global__ void __launch_bounds__(256) split_stats_kernel(const float* __restrict__ logits, int64_t ld, int64_t T,
                                                           int V, int n_splits, HeadPart* __restrict__ part) {
+  after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (i >= T * n_splits) return;
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* __restric
 // Logits -> s (q (A + B (l - lse)) + entries) in place, one block per token.
 __global__ void __launch_bounds__(256) grad_rows_kernel(float* __restrict__ logits, int64_t ld, int V,
                                                         const HeadEntries en, int64_t t0, int64_t T, int n_splits) {
+  after_previous();
   const int64_t t = t0 + blockIdx.x;
   float* row = logits + static_cast<int64_t>(blockIdx.x) * ld;
   const float4 ri = en.row[t];
@@ -190,10 +195,8 @@ cudaError_t head_simt_logits(const HeadProblem& p, int64_t t0, int64_t Tb, float
                                       nullptr, p.T, st);
   if (err != cudaSuccess || part == nullptr) return err;
   const int64_t n = head_splits(p.V);
-  split_stats_kernel<<<static_cast<unsigned>((Tb * n + 7) / 8), 256, 0, st>>>(logits, ld, Tb, static_cast<int>(p.V),
-                                                                              static_cast<int>(n), part);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(split_stats_kernel, dim3(static_cast<unsigned>((Tb * n + 7) / 8)), 256, 0, st, logits, ld, Tb,
+                     static_cast<int>(p.V), static_cast<int>(n), part);
 }
 
 cudaError_t head_simt_backward(const HeadProblem& p, const HeadEntries& en, float* dh, float* dW, int accumulate,
@@ -204,9 +207,9 @@ cudaError_t head_simt_backward(const HeadProblem& p, const HeadEntries& en, floa
     const int64_t n = t0 + Tb <= p.T ? Tb : p.T - t0;
     cudaError_t err = head_simt_logits(p, t0, n, logits, ld, nullptr, st);
     if (err != cudaSuccess) return err;
-    grad_rows_kernel<<<static_cast<unsigned>(n), 256, 0, st>>>(logits, ld, static_cast<int>(p.V), en, t0, p.T,
-                                                               static_cast<int>(head_splits(p.V)));
-    note_launches(1);
+    err = head_launch(grad_rows_kernel, dim3(static_cast<unsigned>(n)), 256, 0, st, logits, ld, static_cast<int>(p.V),
+                      en, t0, p.T, static_cast<int>(head_splits(p.V)));
+    if (err != cudaSuccess) return err;
     if (dh != nullptr) {
       err = sgemm<true, false>(logits, ld, W, p.D, dh + t0 * p.D, p.D, n, p.D, p.V, 0, nullptr, p.T, st);
       if (err != cudaSuccess) return err;
@@ -217,7 +220,7 @@ cudaError_t head_simt_backward(const HeadProblem& p, const HeadEntries& en, floa
       if (err != cudaSuccess) return err;
     }
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace mls

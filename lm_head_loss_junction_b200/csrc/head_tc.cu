@@ -112,6 +112,7 @@ struct CopyJobs {
 };
 
 __global__ void __launch_bounds__(256) head_copy_kernel(const CopyJobs jobs) {
+  after_previous();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   copy_part(blockIdx.y == 0 ? jobs.w : jobs.h, first, static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(256) head_copy_kernel(const CopyJobs jobs) {
 // The copy again with a power-of-two scale when the largest magnitude is at or
 // past 2^15 or below 2^-10; the reciprocal of the scale for the epilogue.
 __global__ void __launch_bounds__(256) head_rescale_kernel(const CopyJobs jobs) {
+  after_previous();
   const CopyArgs& a = blockIdx.y == 0 ? jobs.w : jobs.h;
   if (a.n_vec == 0) return;
   const float mx = __uint_as_float(*a.maxbits);
@@ -260,6 +262,22 @@ struct RowAhead {
   float4 ri;                       // (lse, A, B, s)
 };
 
+// A warp's 32 x 32 fp32 chunk in its staging rows: 16-byte pieces permuted by
+// row, so that rows and columns of pieces are free of bank conflicts.
+__device__ __forceinline__ float4* staged(uint8_t* stage, int row, int piece) {
+  return reinterpret_cast<float4*>(stage + row * 128 + ((piece ^ (row & 7)) * 16));
+}
+
+__device__ __forceinline__ float* staged_at(uint8_t* stage, int row, int col) {
+  return reinterpret_cast<float*>(staged(stage, row, col >> 2)) + (col & 3);
+}
+
+// This lane's row.  (Only a __syncwarp makes it visible to other lanes.)
+__device__ __forceinline__ void stage_row(uint8_t* stage, int lane, const float (&r)[32]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) *staged(stage, lane, k) = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+}
+
 // A_MN / B_MN: the operand is stored with its M / N dimension contiguous
 // (boxes of 64 x 64), otherwise with K contiguous.
 template <Epi EPI>
@@ -284,7 +302,6 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       release();
       return;
     }
-    const int t = static_cast<int>(row);
     const int split = c0 / kHeadSplit;
     EntryWalk& en = ahead.en;
     float top = -INFINITY, m = -INFINITY, z = 0.f, u = 0.f;
@@ -296,16 +313,14 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       const int col = c0 + c * 32;
       if (col >= a.cols) continue;
       if constexpr (EPI == kStats) {
-        while (__any_sync(0xffffffffu, en.cur.x < col + 32)) {
-          const bool mine = en.cur.x < col + 32;
-          const int k0 = mine ? en.cur.x - col : -1;
-          float v = 0.f;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v = k == k0 ? r[k] : v;
-          if (mine) {
-            a.picked[static_cast<int64_t>(t) * a.Ntot + en.cur.y] = v;
+        if (__any_sync(0xffffffffu, en.cur.x < col + 32)) {
+          // a register array cannot be indexed: each lane reads its row back
+          stage_row(s.stage[warp - 2], lane, r);
+          while (en.cur.x < col + 32) {
+            a.picked[row * a.Ntot + en.cur.y] = *staged_at(s.stage[warp - 2], lane, en.cur.x - col);
             en.next();
           }
+          __syncwarp();
         }
       }
       mask_columns(r, a.cols - col);
@@ -336,20 +351,16 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
       u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
       if constexpr (EPI == kLogits) {
-        // through the warp's staging rows (16-byte pieces permuted by row, so that both sides are free of bank
-        // conflicts): a store instruction writes 4 rows x 128 contiguous bytes
+        // through the staging rows: a store instruction writes 4 rows x 128 contiguous bytes
         uint8_t* stage = s.stage[warp - 2];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) * 16)) =
-              make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        stage_row(stage, lane, r);
         __syncwarp();
         const int64_t row0 = row - lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int rr = i * 4 + (lane >> 3), ch = lane & 7;
-          const float4 v = *reinterpret_cast<const float4*>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
-          if (row0 + rr < a.rows) *reinterpret_cast<float4*>(a.logits + (row0 + rr) * a.ld + col + ch * 4) = v;
+          if (row0 + rr < a.rows)
+            *reinterpret_cast<float4*>(a.logits + (row0 + rr) * a.ld + col + ch * 4) = *staged(stage, rr, ch);
         }
         __syncwarp();
       }
@@ -384,13 +395,21 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
 #pragma unroll
         for (int k = 0; k < 32; ++k) r[k] = live && k < left ? r[k] : 0.f;
       }
-      while (__any_sync(0xffffffffu, en.cur.x - a.v0 < col + 32)) {
-        const bool mine = en.cur.x - a.v0 < col + 32;
-        const int k0 = mine ? en.cur.x - a.v0 - col : -1;
-        const float cf = __int_as_float(en.cur.y);
+      if (__any_sync(0xffffffffu, en.cur.x - a.v0 < col + 32)) {
+        stage_row(stage, lane, r);
+        while (en.cur.x - a.v0 < col + 32) {
+          *staged_at(stage, lane, en.cur.x - a.v0 - col) += __int_as_float(en.cur.y);
+          en.next();
+        }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) r[k] += k == k0 ? cf : 0.f;
-        if (mine) en.next();
+        for (int k = 0; k < 8; ++k) {
+          const float4 v = *staged(stage, lane, k);
+          r[4 * k] = v.x;
+          r[4 * k + 1] = v.y;
+          r[4 * k + 2] = v.z;
+          r[4 * k + 3] = v.w;
+        }
+        __syncwarp();                      // the rows below lie across these
       }
       uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStageRow);
 #pragma unroll
@@ -412,52 +431,51 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     float alpha = inv;
     if constexpr (EPI == kDw) alpha = inv * __uint_as_float(__ldg(a.smax));
     const float rs = EPI == kDh && valid ? __ldg(&a.row[row].w) : 1.f;
+    uint8_t* stage = s.stage[warp - 2];
+    const int64_t row0 = row - lane;
+    const int rr0 = lane >> 3, ch = lane & 7;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float r[32];
       tmem_ld32(acc_col + c * 32, r);
       if (c == 3) release();
       const int col = c0 + c * 32;
-      if (!valid || col >= a.cols) continue;
-      const int64_t off = row * a.cols + col;
+      if (col >= a.cols) continue;
 #pragma unroll
       for (int k = 0; k < 32; ++k) r[k] *= alpha;
-      if constexpr (OUT_BF16) {
-        if (EPI == kDh && a.acc != nullptr) {
-          const float4* ad = reinterpret_cast<const float4*>(a.acc + off);
+      stage_row(stage, lane, r);
+      __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 v = ad[k];
-            r[4 * k] += v.x;
-            r[4 * k + 1] += v.y;
-            r[4 * k + 2] += v.z;
-            r[4 * k + 3] += v.w;
-          }
-        }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = r[8 * k + i] * rs;
-          dst[k] = f32_to_bf16x8(f);
-        }
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
-                                                static_cast<int64_t>(part) * a.rows * a.cols + off);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float4 v = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-          if (a.accumulate) {
-            const float4 o = dst[k];
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + rr0;
+        const float scale = __shfl_sync(0xffffffffu, rs, rr);
+        if (row0 + rr >= a.rows) continue;
+        const int64_t off = (row0 + rr) * a.cols + col + ch * 4;
+        float4 v = *staged(stage, rr, ch);
+        if constexpr (OUT_BF16) {
+          if (EPI == kDh && a.acc != nullptr) {
+            const float4 o = *reinterpret_cast<const float4*>(a.acc + off);
             v.x += o.x;
             v.y += o.y;
             v.z += o.z;
             v.w += o.w;
           }
-          dst[k] = v;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off) =
+              make_uint2(pack_bf16x2(v.x * scale, v.y * scale), pack_bf16x2(v.z * scale, v.w * scale));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
+                                                  static_cast<int64_t>(part) * a.rows * a.cols + off);
+          if (a.accumulate) {
+            const float4 o = *dst;
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
+          *dst = v;
         }
       }
+      __syncwarp();
     }
   }
 }
@@ -502,6 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
   cluster_sync_all();        // every barrier of both CTAs exists before any remote arrive
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
+  after_previous();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -636,18 +655,34 @@ struct ReduceArgs {
   uint2* out;                      // bf16, or NULL: the sums go to acc
 };
 
+// Eight lanes per output, each with every eighth part; their sums meet in a
+// fixed order.
+constexpr int kReduceLanes = 8;
+
 __global__ void __launch_bounds__(256) head_reduce_kernel(const ReduceArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.n) return;
-  float4 v = a.acc_in ? a.acc[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+  after_previous();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kReduceLanes;
+  const int own = threadIdx.x % kReduceLanes;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < a.n) {
+    if (own == 0 && a.acc_in) v = a.acc[i];
 #pragma unroll 4
-  for (int p = 0; p < a.parts; ++p) {
-    const float4 x = __ldg(a.part + p * a.n + i);
-    v.x += x.x;
-    v.y += x.y;
-    v.z += x.z;
-    v.w += x.w;
+    for (int p = own; p < a.parts; p += kReduceLanes) {
+      const float4 x = __ldg(a.part + p * a.n + i);
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+    }
   }
+#pragma unroll
+  for (int o = kReduceLanes / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  if (i >= a.n || own != 0) return;
   if (a.out == nullptr) {
     a.acc[i] = v;
     return;
@@ -760,9 +795,7 @@ cudaError_t run_tiles(const TileMaps& maps, TileArgs a, int64_t kdim, int parts,
   if (err != cudaSuccess) return err;
   const int resident = resident_pairs<EPI, OUT_BF16>();
   const int pairs = a.units < resident ? a.units : resident;
-  fn<<<2 * pairs, threads_of<EPI>(), kSmemBytes, st>>>(maps, a);
-  note_launches(1);
-  return cudaGetLastError();
+  return head_launch(fn, dim3(static_cast<unsigned>(2 * pairs)), threads_of<EPI>(), kSmemBytes, st, maps, a);
 }
 
 // Parts of dh's K: dh has ceil(T / 256) ceil(D / 256) tiles, few when T is
@@ -887,8 +920,8 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
   q += w.h16;
   __half* w16 = reinterpret_cast<__half*>(q);
   q += w.w16;
-  unsigned int* maxbits = reinterpret_cast<unsigned int*>(q);          // [0] W, [1] h
-  float* inv = reinterpret_cast<float*>(q + 64);
+  unsigned int* maxbits = en.smax + 1;               // [0] W, [1] h; 0 from the entries' launch
+  float* inv = reinterpret_cast<float*>(q);
   cudaError_t err = cudaSuccess;
   // From 2048 tokens on the tensor pipe bounds the G' kernel and two more warps of it make the fp16 copies
   // unnoticed (they move 0.6 TB/s; a kernel of their own before it cost 48 us at V = 49152, D = 1024, of 2.9 ms);
@@ -902,13 +935,13 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     if (dh != nullptr) set_copy(copy.w, Wc, w16, n, p.D, nullptr, maxbits, inv);
     if (dW != nullptr && first) set_copy(copy.h, p.h, h16, p.T, p.D, &en, maxbits + 1, inv + 1);
     const bool any = copy.w.n_vec > 0 || copy.h.n_vec > 0;
-    if (any) {
-      err = cudaMemsetAsync(maxbits, 0, (first ? 2 : 1) * sizeof(unsigned int), st);
+    if (any && !first) {
+      err = cudaMemsetAsync(maxbits, 0, sizeof(unsigned int), st);
       if (err != cudaSuccess) return err;
     }
     if (any && !beside) {
-      head_copy_kernel<<<copy_grid(copy), 256, 0, st>>>(copy);
-      note_launches(1);
+      err = head_launch(head_copy_kernel, copy_grid(copy), 256, 0, st, copy);
+      if (err != cudaSuccess) return err;
     }
     TileMaps maps;
     TileArgs a{};
@@ -931,8 +964,8 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     err = run_tiles<kGrad, false>(maps, a, p.D, 1, st);
     if (err != cudaSuccess) return err;
     if (any) {
-      head_rescale_kernel<<<copy_grid(copy), 256, 0, st>>>(copy);
-      note_launches(1);
+      err = head_launch(head_rescale_kernel, copy_grid(copy), 256, 0, st, copy);
+      if (err != cudaSuccess) return err;
     }
     if (dh != nullptr) {
       TileArgs d{};
@@ -957,9 +990,8 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
         r.acc_in = first ? 0 : 1;
         r.row = en.row;
         r.out = last ? static_cast<uint2*>(dh) : nullptr;
-        head_reduce_kernel<<<static_cast<unsigned>((r.n + 255) / 256), 256, 0, st>>>(r);
-        note_launches(1);
-        err = cudaGetLastError();
+        err = head_launch(head_reduce_kernel, dim3(static_cast<unsigned>((r.n * kReduceLanes + 255) / 256)), 256, 0, st,
+                          r);
       } else if (last) {
         d.out = dh;
         d.acc = first ? nullptr : acc;
