@@ -124,6 +124,9 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
   f.ldT = p.T;
   f.n_splits = static_cast<int>(head_splits(p.V));
   f.part = part;
+  f.log2e = !p.bf16 ? mls::head_log2e(0, 1)
+            : p.T <= mls::kFewTokens ? mls::head_log2e(p.D, mls::head_few_parts(mls::head_few_width(p.T)))
+                                     : mls::head_log2e(p.D, 1);
   f.logits = logits;
   f.ld = plan.ld;
   f.picked = plan.store ? nullptr : picked;

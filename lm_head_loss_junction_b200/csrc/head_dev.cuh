@@ -14,8 +14,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// l log2(e) - m, rounded once.
-__device__ __forceinline__ float to_base2(float l, float m) { return fmaf(l, kLog2e, -m); }
+// l log2(e) - m, rounded once (log2e: head_log2e of the product that made l).
+__device__ __forceinline__ float to_base2(float l, float log2e, float m) { return fmaf(l, log2e, -m); }
 
 // The kernels of one call are launched so that the next may be set up while one
 // runs; each thread waits here, before its first access to global memory, until

@@ -39,12 +39,13 @@ struct FewArgs {
   HeadPart* part;                  // [T][n_tiles]
   float* logits;                   // [T][ld]
   int64_t ld;
+  float log2e;
   int32_t* status;
 };
 
 template <int TN>
 struct Few {
-  static constexpr int kAcc = TN <= 32 ? 8 : 256 / TN;               // accumulators per buffer
+  static constexpr int kAcc = head_few_parts(TN);                    // accumulators per buffer
   static constexpr int kCols = 2 * kAcc * TN;                        // TMEM columns: two buffers
   static constexpr int kPad = kRows + 4;
   static constexpr int kStageBytes = kRows * kBK * 2 + TN * kBK * 2;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
 #pragma unroll
           for (int o = kSub / 2; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
           if (cm > top) {
-            const float next = cm * kLog2e;
+            const float next = cm * a.log2e;
             if (z > 0.f) {
               const float d = m - next, f = ex2(d);
               u = f * fmaf(d, z, u);
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
           }
 #pragma unroll
           for (int k = 0; k < kChunk; ++k) {
-            const float d = to_base2(l[k], m), x = ex2(d);
+            const float d = to_base2(l[k], a.log2e, m), x = ex2(d);
             z += x;
             u = fmaf(d, x, u);
           }
@@ -275,7 +276,7 @@ cudaError_t run_few(const FewMaps& maps, const FewArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t head_tc_few(const HeadProblem& p, const HeadForward& f, cudaStream_t st) {
-  const int tn = f.T <= 16 ? 16 : f.T <= 32 ? 32 : f.T <= 64 ? 64 : 128;
+  const int tn = head_few_width(f.T);
   FewMaps maps;
   if (!head_make_map(&maps.w, p.W, p.D, p.V, p.D, kBK, kRows, false)) return cudaErrorInvalidValue;
   if (!head_make_map(&maps.h, f.h, p.D, f.T, p.D, kBK, tn, false)) return cudaErrorInvalidValue;
@@ -287,6 +288,7 @@ cudaError_t head_tc_few(const HeadProblem& p, const HeadForward& f, cudaStream_t
   a.part = f.part;
   a.logits = f.logits;
   a.ld = f.ld;
+  a.log2e = head_log2e(p.D, head_few_parts(tn));
   a.status = p.status;
   switch (tn) {
     case 16: return run_few<16>(maps, a, st);

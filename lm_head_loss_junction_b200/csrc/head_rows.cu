@@ -240,7 +240,7 @@ __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int
       const int id = ids[j];
       const bool there = id >= 0 && id < f.V;
       float d = 0.f;
-      if (there) d = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, f.N, j, id), m);
+      if (there) d = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, f.N, j, id), f.log2e, m);
       f.logp[t * f.N + j] = there ? kLn2 * (d - logz) : 0.f;
       bad |= !there && id != -1;
     }
@@ -266,13 +266,13 @@ __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int
         if (id < 0 || id >= f.V) continue;
         const float p = expf(f.teacher[t * f.N + j] - top);
         sum += p;
-        if (p != 0.f) kd = fmaf(p, logz - to_base2(entry_logit(f, t, tot, j, id), m), kd);
+        if (p != 0.f) kd = fmaf(p, logz - to_base2(entry_logit(f, t, tot, j, id), f.log2e, m), kd);
       }
     sum = warp_sum(sum);
     kd = warp_sum(kd);
     kd = some && !out ? kLn2 * (kd / sum) : 0.f;
     if (lane == 0) {
-      const float ce = out ? 0.f : kLn2 * (logz - to_base2(entry_logit(f, t, tot, f.N, y), m));
+      const float ce = out ? 0.f : kLn2 * (logz - to_base2(entry_logit(f, t, tot, f.N, y), f.log2e, m));
       f.stats[f.ldT + t] = ce;
       f.stats[2 * f.ldT + t] = kd;
       const bool counts = !out && w != 0.f;  // 0 times a term that is not a number is not 0
@@ -319,10 +319,9 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
 // candidates are multiplied once more with every product exact and added in 64
 // bits; then only equal logits tie, and the lower id comes first.
 //
-// The tensor cores' accumulation truncates, which shrinks a logit by about
-// D 1e-9 of itself (2e-6 at D = 2304); the candidates' terms of z and u, the
-// ones that weigh, are replaced by those of these products, and so are the
-// given tokens' logits.
+// The candidates' terms of z and u, the ones that weigh, are replaced by those
+// of these products, which are more exact than the tensor cores' sums, and so
+// are the given tokens' logits.
 //
 // The selection is a chain of short dependent steps (a block takes about 8 us
 // for a token whatever the sizes), several blocks per SM hide each other's; the
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   }
   const int rank = r < have ? s.rank[r] : 0;
   if (r < have) {
-    const float was = to_base2(s.tile[r], m), is = fine_base2(fine[r], m);
+    const float was = to_base2(s.tile[r], f.log2e, m), is = fine_base2(fine[r], m);
     const float e0 = ex2(was), e1 = ex2(is);
     s.dz[rank] = e1 - e0;
     s.du[rank] = is * e1 - was * e0;

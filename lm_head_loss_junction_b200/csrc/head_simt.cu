@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* __restric
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (c0 + k * 32 + lane >= V) continue;
-    const float d = to_base2(l[k], m), e = ex2(d);
+    const float d = to_base2(l[k], kLog2e, m), e = ex2(d);
     z += e;
     u = fmaf(d, e, u);
   }
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(float* __restrict__ logi
   float* row = logits + static_cast<int64_t>(blockIdx.x) * ld;
   const float4 ri = en.row[t];
   for (int v = threadIdx.x; v < V; v += 256) {
-    const float d = to_base2(row[v], ri.x * kLog2e);
+    const float d = to_base2(row[v], kLog2e, ri.x * kLog2e);
     row[v] = ri.w == 0.f ? 0.f : ri.w * (ex2(d) * fmaf(ri.z * kLn2, d, ri.y));
   }
   __syncthreads();

@@ -151,6 +151,7 @@ struct TileArgs {
   int units;
   // stats, logits, grad
   int v0;                          // vocabulary id of column 0
+  float log2e;                     // of the logits
   int n_splits;                    // splits of a row of part
   HeadPart* part;
   float* logits;
@@ -331,7 +332,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       const float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
       if (cm > top) {
         // move the sums to the new reference: with d = m - m', a' = a + d, 2^a' = 2^d 2^a
-        const float next = cm * kLog2e;
+        const float next = cm * a.log2e;
         if (z > 0.f) {
           const float d = m - next, f = ex2(d);
           u = f * fmaf(d, z, u);
@@ -343,7 +344,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       float z4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float d = to_base2(r[k], m);
+        const float d = to_base2(r[k], a.log2e, m);
         const float e = ex2(d);
         z4[k & 3] += e;
         u4[k & 3] = fmaf(d, e, u4[k & 3]);
@@ -388,7 +389,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       const int left = a.cols - col;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float d = to_base2(r[k], lse2);
+        const float d = to_base2(r[k], a.log2e, lse2);
         r[k] = ex2(d) * fmaf(B2, d, A);
       }
       if (!all_live || left < 32) {
@@ -877,6 +878,7 @@ cudaError_t head_tc_forward(const HeadProblem& p, const HeadForward& f, cudaStre
   a.cols = static_cast<int>(p.V);
   a.n_splits = static_cast<int>(head_splits(p.V));
   a.part = f.part;
+  a.log2e = head_log2e(p.D, 1);
   a.logits = f.logits;
   a.ld = f.ld;
   a.e = f.en.e;
@@ -952,6 +954,7 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     a.rows = static_cast<int>(p.T);
     a.cols = static_cast<int>(n);
     a.v0 = static_cast<int>(v0);
+    a.log2e = head_log2e(p.D, 1);
     a.e = en.e;
     a.first = en.first;
     a.ld_first = p.T;
