@@ -524,7 +524,7 @@ constexpr int kBins = 256;
 struct TopSmem {
   int hist[kBins];
   int chosen[4];
-  float part[32][3];
+  float part[32][2];                         // sums z and u of each warp's splits
   float h2;
   unsigned int w2;                           // largest squared norm of a candidate's row, as bits
   int count, n_sel, border;
@@ -572,24 +572,26 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     largest = fmaxf(largest, p.w);
     merge_part(m, z, u, p.x, p.y, p.z);
   }
-  warp_merge(m, z, u);
   largest = warp_max(largest);
-  if (lane == 0) {
-    s.part[warp][0] = m;
-    s.part[warp][1] = z;
-    s.part[warp][2] = u;
-    s.dz[warp] = largest;
-  }
+  if (lane == 0) s.dz[warp] = largest;
   __syncthreads();
-  m = -INFINITY, z = 0.f, u = 0.f, largest = -INFINITY;
-  if (lane < kWarps) {
-    m = s.part[lane][0];
-    z = s.part[lane][1];
-    u = s.part[lane][2];
-    largest = s.dz[lane];
+  largest = warp_max(lane < kWarps ? s.dz[lane] : -INFINITY);
+  {
+    // one reference for the block: that of the split with the largest logit
+    const float ref = largest * f.log2e;
+    if (z > 0.f || z != z) {
+      const float d = m - ref, e = ex2(d);
+      u = e * fmaf(d, z, u);
+      z *= e;
+    }
+    m = ref;
+    z = warp_sum(z);
+    u = warp_sum(u);
+    if (lane == 0) {
+      s.part[warp][0] = z;
+      s.part[warp][1] = u;
+    }
   }
-  warp_merge(m, z, u);
-  largest = warp_max(largest);
 
   // the border bin of the maxima, the splits on this side of it, their logits on this side of it
   // (with fewer splits than candidates, the border of the logits themselves)
@@ -729,6 +731,8 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   }
   __syncthreads();
   if (warp * 32 >= kMaxEntries + kTopMore) return;
+  z = warp_sum(lane < kWarps ? s.part[lane][0] : 0.f);
+  u = warp_sum(lane < kWarps ? s.part[lane][1] : 0.f);
   float dz = 0.f, du = 0.f;
   for (int i = lane; i < have; i += 32) {
     dz += s.dz[i];
@@ -796,14 +800,18 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const int list = padded < 1024 ? static_cast<int>(padded) : 1024;
   const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t) +
                       static_cast<size_t>(f.n_splits) * 8;
-  // Few tokens leave SMs idle: their blocks get all the warps that help.  (T = 1, D = 2304, K = 8: 24 us with 256
-  // threads, 15 with 1024.)  Many tokens share an SM: 256 threads, several blocks.
+  // Few tokens leave SMs idle: their blocks get all the warps that help (T = 1, D = 2304, K = 8: 24 us with 256
+  // threads, 15 with 1024).
   const bool wide = f.T <= 148;
-  auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : head_top_kernel<true, 256>)
-                   : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 256>);
+  // Of many tokens small blocks are best, more of them in flight per SM, until the products outweigh the steps before
+  // them (T = 4096, K = 32, with 128 and 256 threads: D = 64 103 and 120 us, 512 114 and 127, 2304 285 and 266).
+  const bool light = static_cast<int64_t>(C + f.N) * f.D <= 40000;
+  auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : light ? head_top_kernel<true, 128> : head_top_kernel<true, 256>)
+                   : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 128>);
+  const unsigned threads = wide ? 1024 : light || !f.bf16 ? 128 : 256;
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  return head_launch(fn, dim3(static_cast<unsigned>(f.T)), wide ? 1024u : 256u, smem, st, f, C, list);
+  return head_launch(fn, dim3(static_cast<unsigned>(f.T)), threads, smem, st, f, C, list);
 }
 
 }  // namespace mls

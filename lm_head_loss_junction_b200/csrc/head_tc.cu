@@ -95,12 +95,12 @@ __device__ __forceinline__ void copy_part(const CopyArgs& a, int64_t first, int6
   const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
   float mx = 0.f;
   int64_t i = first;
-  for (; i + 3 * stride < a.n_vec; i += 4 * stride) {
-    uint4 v[4];
+  for (; i + 7 * stride < a.n_vec; i += 8 * stride) {
+    uint4 v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldg(a.src + i + k * stride);
+    for (int k = 0; k < 8; ++k) v[k] = __ldg(a.src + i + k * stride);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
+    for (int k = 0; k < 8; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
   }
   for (; i < a.n_vec; i += stride) a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax), mx);
   mx = warp_max(mx);
@@ -257,7 +257,8 @@ struct EntryWalk {
 };
 
 // What a row of a tile needs besides its accumulator, loaded before the
-// epilogue waits for the accumulator so that the loads' latency is hidden.
+// epilogue waits for the accumulator.  (Asking a whole tile ahead measured
+// slower: 2.91 against 2.86 ms for the step at T = 8192, D = 1024, 64 entries.)
 struct RowAhead {
   EntryWalk en;
   float4 ri;                       // (lse, A, B, s)
@@ -615,11 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
       RowAhead ahead;
       if constexpr (EPI == kStats || EPI == kGrad) {
         const int c0 = u.nt * kBN + half * 128;
-        const bool here = row < a.rows && c0 < a.cols;
-        const int t = static_cast<int>(row);
-        if constexpr (EPI == kGrad) ahead.ri = row < a.rows ? __ldg(a.row + t) : make_float4(0.f, 0.f, 0.f, 0.f);
-        // a row of scale 0 has entries, of coefficient 0: its G' is 0 whatever the row holds
-        ahead.en.start(a, here, t, (a.v0 + c0) / kHeadSplit);
+        if constexpr (EPI == kGrad) ahead.ri = row < a.rows ? __ldg(a.row + row) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // (a row of scale 0 has entries, of coefficient 0: its G' is 0 whatever the row holds)
+        ahead.en.start(a, row < a.rows && c0 < a.cols, static_cast<int>(row), (a.v0 + c0) / kHeadSplit);
       }
       if (!warp_wait(&s.tfull[buf], (iter >> 1) & 1, abort, a.status)) break;
       tc_fence_after();
@@ -925,10 +924,11 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
   unsigned int* maxbits = en.smax + 1;               // [0] W, [1] h; 0 from the entries' launch
   float* inv = reinterpret_cast<float*>(q);
   cudaError_t err = cudaSuccess;
-  // From 2048 tokens on the tensor pipe bounds the G' kernel and two more warps of it make the fp16 copies
-  // unnoticed (they move 0.6 TB/s; a kernel of their own before it cost 48 us at V = 49152, D = 1024, of 2.9 ms);
-  // below, reading W bounds it and the copies would prolong it.
-  const bool beside = p.T >= 2048;
+  // From 512 tokens on the tensor pipe bounds the G' kernel and two more warps of it make the fp16 copies beside it;
+  // below, reading W bounds it and the copies, in so few threads, would prolong it.  Whole steps, V = 32771, D = 1024,
+  // copies beside it and before it in a kernel of their own: T = 300 215 and 201 us, 777 265 and 278, 1200 329 and
+  // 354, 2047 530 and 535.
+  const bool beside = p.T >= 512;
   for (int64_t v0 = 0; v0 < p.V; v0 += Vc) {
     const int64_t n = v0 + Vc <= p.V ? Vc : p.V - v0;
     const bool first = v0 == 0, last = v0 + n >= p.V;
