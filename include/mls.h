@@ -463,7 +463,8 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  * Common arguments
  *   T, D, V    tokens, width, vocabulary.  MLS_BF16 needs D % 64 == 0; V is
  *              any size.  MLS_F32 accepts any sizes (CUDA-core path).
- *   h, W       device dt [T, D] and dt [V, D], 16-byte aligned
+ *   h, W       device dt [T, D] and dt [V, D]; 16-byte aligned with MLS_BF16 (dh
+ *              and dW too), 4-byte with MLS_F32
  *   ids        device int32; -1 means "no token there" (its outputs are 0, it
  *              has no gradient); any other value outside [0, V) is treated the
  *              same and sets MLS_DEVFLAG_BAD_ID
@@ -471,15 +472,16 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  *   dW         device [V, D] of dW_dt, or NULL (a frozen head): MLS_F32, added
  *              to with accumulate_dW != 0, or (with MLS_BF16 inputs) MLS_BF16,
  *              rounded once from the fp32 sum; MLS_BF16 with accumulate_dW is
- *              MLS_ERR_UNSUPPORTED.  dh and dW must not both be NULL.
+ *              MLS_ERR_UNSUPPORTED.  dh and dW must not both be NULL, and no
+ *              output may overlap an input.
  *   workspace  device, 16-byte aligned.  The queries give the size that works
  *              in one piece, or within 1.5 GiB in pieces; any size of at least
  *              the minimum (each min pointer may be NULL) is accepted, and a
  *              smaller one means more pieces.  Nothing in it is kept from call
  *              to call; two calls that may overlap on the GPU (two captured
  *              graphs among them) need one each.
- * Results are deterministic for a given workspace size (no floating-point
- * atomics).
+ * Results are deterministic (no floating-point atomics); dh and dW may differ in
+ * the last bits between workspace sizes, the other results do not.
  */
 
 /*
@@ -513,8 +515,9 @@ mls_status mls_token_logprobs(int64_t T, int64_t D, int64_t V, int N, const int3
  *   dL/dl_v = -q_v (sum_n g_n + e (log q_v + entropy)) + sum over ids_n = v of g_n
  *   dh = dL/dl W,  dW (+)= dL/dl^T h
  *   stats      the forward call's, for the same h and W
- *   g_logp     device f32 [T, N], 1 <= N <= 64 (entries without a token are not read as gradients)
- *   g_entropy  device f32 [T] or NULL (0)
+ *   g_logp     device f32 [T, N], 1 <= N <= 64, finite (entries without a token
+ *              are not read as gradients)
+ *   g_entropy  device f32 [T], finite, or NULL (0)
  * The alternatives are given tokens too: pass their ids and gradients.
  * MLS_BF16: dL/dl is formed in fp16 (11-bit significand, each row over a power
  * of two near its largest coefficient) for one chunk of the vocabulary at a

@@ -87,6 +87,7 @@ cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bo
 // ------------------------------------------------------------------ per-token results
 struct HeadFinish {
   int64_t T, V;                    // tokens of this launch
+  int64_t all;                     // of the whole call (no result depends on the pieces)
   int64_t ldT;                     // row stride of the [*][T] outputs
   int n_splits;
   const HeadPart* part;            // [T][n_splits]

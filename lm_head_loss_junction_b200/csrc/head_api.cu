@@ -121,6 +121,7 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
   float* logits = plan.store ? reinterpret_cast<float*>(q) : nullptr;
   const size_t esize = p.bf16 ? 2 : 4;
   f.V = p.V;
+  f.all = p.T;
   f.ldT = p.T;
   f.n_splits = static_cast<int>(head_splits(p.V));
   f.part = part;
@@ -215,9 +216,12 @@ mls_status backward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, voi
                                            reinterpret_cast<float*>(rest), simt_block(p, ws_bytes - e), st));
 }
 
+// 16-byte loads and stores, or single fp32 values on the CUDA-core path.
+uintptr_t alignment(mls_dtype dt) { return dt == MLS_BF16 ? 16 : 4; }
+
 mls_status check_backward(const void* dh, const void* dW, mls_dtype dt, mls_dtype dW_dt, int accumulate_dW) {
   if (dh == nullptr && dW == nullptr) return MLS_ERR_INVALID_ARG;
-  if (!aligned(dh, 16) || !aligned(dW, 16)) return MLS_ERR_UNSUPPORTED;
+  if (!aligned(dh, alignment(dt)) || !aligned(dW, alignment(dt))) return MLS_ERR_UNSUPPORTED;
   if (dW != nullptr) {
     if (dW_dt != MLS_F32 && dW_dt != MLS_BF16) return MLS_ERR_INVALID_ARG;
     if (dW_dt == MLS_BF16 && dt != MLS_BF16) return MLS_ERR_UNSUPPORTED;
@@ -227,9 +231,9 @@ mls_status check_backward(const void* dh, const void* dW, mls_dtype dt, mls_dtyp
   return MLS_OK;
 }
 
-mls_status check_operands(const void* h, const void* W) {
+mls_status check_operands(const void* h, const void* W, mls_dtype dt) {
   if (h == nullptr || W == nullptr) return MLS_ERR_INVALID_ARG;
-  return aligned(h, 16) && aligned(W, 16) ? MLS_OK : MLS_ERR_UNSUPPORTED;
+  return aligned(h, alignment(dt)) && aligned(W, alignment(dt)) ? MLS_OK : MLS_ERR_UNSUPPORTED;
 }
 
 mls_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -266,7 +270,7 @@ mls_status mls_token_logprobs(int64_t T, int64_t D, int64_t V, int N, const int3
   MLS_TRY(check_shape(T, D, V, dt));
   MLS_TRY(check_top(V, K));
   if (N > mls::kMaxEntries) return MLS_ERR_UNSUPPORTED;
-  MLS_TRY(check_operands(h, W));
+  MLS_TRY(check_operands(h, W, dt));
   if ((N > 0 && (ids == nullptr || logp == nullptr)) || stats == nullptr) return MLS_ERR_INVALID_ARG;
   if (K > 0 && (top_ids == nullptr || top_logp == nullptr)) return MLS_ERR_INVALID_ARG;
   if (!aligned(ids, 4) || !aligned(logp, 4) || !aligned(stats, 4) || !aligned(top_ids, 4) || !aligned(top_logp, 4))
@@ -312,7 +316,7 @@ mls_status mls_token_logprobs_bwd(int64_t T, int64_t D, int64_t V, int N, const 
   if (N < 1) return MLS_ERR_INVALID_ARG;
   MLS_TRY(check_shape(T, D, V, dt));
   if (N > mls::kMaxEntries) return MLS_ERR_UNSUPPORTED;
-  MLS_TRY(check_operands(h, W));
+  MLS_TRY(check_operands(h, W, dt));
   if (ids == nullptr || stats == nullptr || g_logp == nullptr) return MLS_ERR_INVALID_ARG;
   if (!aligned(ids, 4) || !aligned(stats, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
     return MLS_ERR_UNSUPPORTED;
@@ -355,7 +359,7 @@ mls_status mls_topk_distill_fwd(int64_t T, int64_t D, int64_t V, int K, const in
   if (K < 1) return MLS_ERR_INVALID_ARG;
   MLS_TRY(check_shape(T, D, V, dt));
   if (K > mls::kMaxEntries) return MLS_ERR_UNSUPPORTED;
-  MLS_TRY(check_operands(h, W));
+  MLS_TRY(check_operands(h, W, dt));
   if (y_targets == nullptr || teacher_ids == nullptr || teacher_logits == nullptr || losses == nullptr ||
       stats == nullptr || !std::isfinite(alpha_d))
     return MLS_ERR_INVALID_ARG;
@@ -400,7 +404,7 @@ mls_status mls_topk_distill_bwd(int64_t T, int64_t D, int64_t V, int K, const in
   if (K < 1) return MLS_ERR_INVALID_ARG;
   MLS_TRY(check_shape(T, D, V, dt));
   if (K > mls::kMaxEntries) return MLS_ERR_UNSUPPORTED;
-  MLS_TRY(check_operands(h, W));
+  MLS_TRY(check_operands(h, W, dt));
   if (y_targets == nullptr || teacher_ids == nullptr || teacher_logits == nullptr || stats == nullptr ||
       !std::isfinite(alpha_d) || !std::isfinite(grad_scale))
     return MLS_ERR_INVALID_ARG;

@@ -520,6 +520,7 @@ __device__ __forceinline__ void block_dots(const void* h, const void* W, int64_t
 }
 
 constexpr int kBins = 256;
+constexpr int kTopSmemLimit = 200 * 1024;
 
 struct TopSmem {
   int hist[kBins];
@@ -802,14 +803,15 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
                       static_cast<size_t>(f.n_splits) * 8;
   // Few tokens leave SMs idle: their blocks get all the warps that help (T = 1, D = 2304, K = 8: 24 us with 256
   // threads, 15 with 1024).
-  const bool wide = f.T <= 148;
+  const bool wide = f.all <= 148;
   // Of many tokens small blocks are best, more of them in flight per SM, until the products outweigh the steps before
   // them (T = 4096, K = 32, with 128 and 256 threads: D = 64 103 and 120 us, 512 114 and 127, 2304 285 and 266).
   const bool light = static_cast<int64_t>(C + f.N) * f.D <= 40000;
   auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : light ? head_top_kernel<true, 128> : head_top_kernel<true, 256>)
                    : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 128>);
   const unsigned threads = wide ? 1024 : light || !f.bf16 ? 128 : 256;
-  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the limit is the same on every call: another host thread's call may set it between here and the launch
+  const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmemLimit);
   if (err != cudaSuccess) return err;
   return head_launch(fn, dim3(static_cast<unsigned>(f.T)), threads, smem, st, f, C, list);
 }

@@ -102,6 +102,14 @@ def test_valid_calls_without_a_gpu_report_no_device():
     assert distill(w=None) == 7 and distill_bwd(w=None, dW_dt=_lib.MLS_BF16) == 7
 
 
+def test_fp32_operands_need_four_bytes():
+    f32 = dict(dt=_lib.MLS_F32, D=33)
+    for call in CALLS:
+        assert call(h=FAKE + 4, **f32) in (0, 7) if not torch.cuda.is_available() else True
+        assert call(h=FAKE + 2, **f32) == UNSUPPORTED and call(W=FAKE + 1, **f32) == UNSUPPORTED
+    assert score_bwd(dh=FAKE + 2, **f32) == UNSUPPORTED and distill_bwd(dW=FAKE + 2, **f32) == UNSUPPORTED
+
+
 def test_workspace_queries():
     bf, f32 = torch.bfloat16, torch.float32
     # without alternatives the logits are never stored: 16 bytes per token and 128 columns, not 4 per logit

@@ -202,6 +202,89 @@ def test_accumulated_and_single_gradients(dtype):
     assert none is None and torch.equal(only_dW, dW)
 
 
+@pytest.mark.parametrize("T", [140, 600])
+def test_one_gradient_alone_equals_both(T):
+    """With the fp16 copies in a kernel of their own (few tokens) and beside the gradient's."""
+    _, x = _distill_inputs(T, 128, 1300, 5, seed=6)
+    _, stats = topk_distill_fwd(*x)
+    dh, dW = topk_distill_bwd(*x, stats, dW_dtype=BF)
+    assert torch.equal(topk_distill_bwd(*x, stats, want_dW=False)[0], dh)
+    assert torch.equal(topk_distill_bwd(*x, stats, want_dh=False, dW_dtype=BF)[1], dW)
+
+
+def test_views_of_fp32_rows():
+    """fp32 rows of odd width start at any 4-byte boundary."""
+    rng, h, W, y = make(40, 7, 90, F32, seed=8)
+    hg, Wg, yg = gpu(h, W, y)
+    whole = token_logprobs(yg, hg, Wg, top_k=3)
+    part = token_logprobs(yg[3:], hg[3:], Wg, top_k=3)
+    assert torch.equal(whole[0][3:], part[0]) and torch.equal(whole[2][3:], part[2])
+    dh, dW = token_logprobs_bwd(yg[3:], hg[3:], Wg, part[1], torch.ones(37, device="cuda"))
+    G = oh.token_logprobs_grad(y[3:, None], h[3:], W, np.ones((37, 1)))
+    check_grads(Bounds(h[3:], W), G, np.ones(37), dh, dW)
+
+
+def test_host_threads_at_once():
+    """Calls of several host threads, on a stream each and with shapes of their own."""
+    import threading
+    shapes = [(200, 64, 700, 4), (30, 128, 40000, 9), (300, 64, 2000, 33), (140, 128, 300, 1)]
+    data = [_distill_inputs(T, D, V, K, seed=20 + K)[1] for T, D, V, K in shapes]
+
+    def work(i):
+        x = data[i]
+        K = shapes[i][3]
+        losses, stats = topk_distill_fwd(*x)
+        return [losses, stats, *topk_distill_bwd(*x, stats), *token_logprobs(x[0], x[3], x[4], top_k=K)]
+
+    ref = [work(i) for i in range(len(shapes))]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(shapes), []
+
+    def run(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i] = work(i)
+            s.synchronize()
+        except Exception as e:                                   # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for r, g in zip(ref, got):
+        assert all(torch.equal(a, b) for a, b in zip(r, g))
+
+
+def test_offsets_past_32_bits():
+    """One piece of more than 2^32 bytes of logits and 2^31 gradient entries equals pieces of it."""
+    T, D, V = 45056, 64, 50021
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn(V, D, generator=g, device="cuda").to(BF) * 0.25
+    h = torch.randn(T, D, generator=g, device="cuda").to(BF)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ref = token_logprobs(ids, h, W, top_k=2)
+    # [partial statistics, 16 bytes per token and split][fp32 logits of all tokens]
+    big = torch.empty(T * (V // 128 + 1) * 16 + T * ((V + 63) // 64 * 64) * 4 + 4096, dtype=torch.uint8, device="cuda")
+    got = token_logprobs(ids, h, W, top_k=2, workspace=big)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    grad = torch.ones(T, device="cuda") / T
+    dh, dW = token_logprobs_bwd(ids, h, W, ref[1], grad, dW_dtype=BF, workspace=big)
+    dh2, dW2 = token_logprobs_bwd(ids, h, W, ref[1], grad, dW_dtype=BF)
+    assert torch.equal(dW, dW2)                       # a chunk of columns or all of them: the same sums over tokens
+    assert (dh.float() - dh2.float()).abs().max() <= 2.0 ** -7 * dh.float().abs().max()
+    # the last rows against the definition
+    l = h[-4:].double() @ W.double().T
+    q = torch.softmax(l, 1)
+    q[torch.arange(4), ids[-4:].long()] -= 1
+    exp = (-q @ W.double()) / T
+    assert (dh[-4:].double() - exp).abs().max() <= 2.0 ** -7 * exp.abs().max()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_equal_logits_rank_by_id(dtype):
     """Repeated rows of W tie exactly; so does a head of zeros."""
