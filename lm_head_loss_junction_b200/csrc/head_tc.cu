@@ -435,7 +435,6 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     const float rs = EPI == kDh && valid ? __ldg(&a.row[row].w) : 1.f;
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
-    const int rr0 = lane >> 3, ch = lane & 7;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float r[32];
@@ -447,26 +446,38 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       for (int k = 0; k < 32; ++k) r[k] *= alpha;
       stage_row(stage, lane, r);
       __syncwarp();
+      if constexpr (OUT_BF16) {
+        // a store instruction writes 8 rows x 64 contiguous bytes
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + rr0;
-        const float scale = __shfl_sync(0xffffffffu, rs, rr);
-        if (row0 + rr >= a.rows) continue;
-        const int64_t off = (row0 + rr) * a.cols + col + ch * 4;
-        float4 v = *staged(stage, rr, ch);
-        if constexpr (OUT_BF16) {
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), ch = lane & 3;
+          const float scale = __shfl_sync(0xffffffffu, rs, rr);
+          if (row0 + rr >= a.rows) continue;
+          const int64_t off = (row0 + rr) * a.cols + col + ch * 8;
+          float4 v[2] = {*staged(stage, rr, 2 * ch), *staged(stage, rr, 2 * ch + 1)};
           if (EPI == kDh && a.acc != nullptr) {
-            const float4 o = *reinterpret_cast<const float4*>(a.acc + off);
-            v.x += o.x;
-            v.y += o.y;
-            v.z += o.z;
-            v.w += o.w;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 o = reinterpret_cast<const float4*>(a.acc + off)[j];
+              v[j].x += o.x;
+              v[j].y += o.y;
+              v[j].z += o.z;
+              v[j].w += o.w;
+            }
           }
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off) =
-              make_uint2(pack_bf16x2(v.x * scale, v.y * scale), pack_bf16x2(v.z * scale, v.w * scale));
-        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off) =
+              make_uint4(pack_bf16x2(v[0].x * scale, v[0].y * scale), pack_bf16x2(v[0].z * scale, v[0].w * scale),
+                         pack_bf16x2(v[1].x * scale, v[1].y * scale), pack_bf16x2(v[1].z * scale, v[1].w * scale));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+          if (row0 + rr >= a.rows) continue;
+          float4 v = *staged(stage, rr, ch);
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
-                                                  static_cast<int64_t>(part) * a.rows * a.cols + off);
+                                                  static_cast<int64_t>(part) * a.rows * a.cols +
+                                                  (row0 + rr) * a.cols + col + ch * 4);
           if (a.accumulate) {
             const float4 o = *dst;
             v.x += o.x;
