@@ -118,25 +118,28 @@ __global__ void __launch_bounds__(256) head_copy_kernel(const CopyJobs jobs) {
 }
 
 // The copy again with a power-of-two scale when the largest magnitude is at or
-// past 2^15 or below 2^-10; the reciprocal of the scale for the epilogue.
-__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyJobs jobs) {
-  after_previous();
-  const CopyArgs& a = blockIdx.y == 0 ? jobs.w : jobs.h;
+// past 2^15 or below 2^-6; the reciprocal of the scale for the epilogue.
+__device__ __forceinline__ void rescale_part(const CopyArgs& a, int64_t first, int64_t stride) {
   if (a.n_vec == 0) return;
   const float mx = __uint_as_float(*a.maxbits);
   float s = 1.f;
-  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 1024.f))) {
+  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 64.f))) {
     int e = 13 - ilogbf(mx);
     e = e < -126 ? -126 : (e > 126 ? 126 : e);
     s = ldexpf(1.f, e);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
+  if (first == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
   if (s == 1.f) return;
   const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
   float unused = 0.f;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.n_vec; i += stride)
+  for (int64_t i = first; i < a.n_vec; i += stride)
     a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax) * s, unused);
+}
+
+__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyJobs jobs) {
+  after_previous();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  rescale_part(blockIdx.y == 0 ? jobs.w : jobs.h, first, static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 struct TileMaps {
@@ -170,7 +173,8 @@ struct TileArgs {
   int accumulate;
   const float* inv;                // device: 1 / scale of the fp16 copy
   const unsigned int* smax;        // device: largest row scale (dw)
-  CopyJobs copy;                   // grad: fp16 copies made by two more warps
+  CopyJobs copy;                   // grad: fp16 copies made by two more warps,
+  int copied;                      // or made already and given their scale by them
   int32_t* status;
 };
 
@@ -639,8 +643,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
   } else if constexpr (EPI == kGrad) {
     // ---------------------------------------------------------------- fp16 copies for dh and dw
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x - kThreads;
-    copy_part(a.copy.w, first, static_cast<int64_t>(gridDim.x) * kCopyThreads);
-    copy_part(a.copy.h, first, static_cast<int64_t>(gridDim.x) * kCopyThreads);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kCopyThreads;
+    if (a.copied) {
+      rescale_part(a.copy.w, first, stride);
+      rescale_part(a.copy.h, first, stride);
+    } else {
+      copy_part(a.copy.w, first, stride);
+      copy_part(a.copy.h, first, stride);
+    }
   }
 
   __syncthreads();
@@ -974,10 +984,11 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     a.G = G;
     a.ld = w.ldg;
     a.gcols = static_cast<int>((n + 63) / 64 * 64);
-    if (beside) a.copy = copy;
+    a.copy = copy;
+    a.copied = beside ? 0 : 1;
     err = run_tiles<kGrad, false>(maps, a, p.D, 1, st);
     if (err != cudaSuccess) return err;
-    if (any) {
+    if (any && beside) {
       err = head_launch(head_rescale_kernel, copy_grid(copy), 256, 0, st, copy);
       if (err != cudaSuccess) return err;
     }

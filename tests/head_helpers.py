@@ -18,11 +18,13 @@ of a partial sum each; a partial sum is at most sum_i |h_i w_i|):
              2^-11 relative, 2^-25 s_t below fp16's normal range (fp32 path: a
              few units, 2^-22 s_t (12 q + q |log q|), instead).
              W and h are copied to fp16: exact but for values below fp16's normal
-             range, off by 2^-25 of the copy, whose largest value M is at least
-             2^-10 (or lifted to 2^13).  W: 2^-25 max(1, 2^-13 M) on sum_v |G_tv|.
-             h is copied times 64 s_t / s_max and meets G / s_t, with the kernel's
-             s_t more than half the one here: 2 s_max 2^-25 max(2^-6, 2^-13 M)
-             on sum_t |G_tv| / s_t.  Summed over k = V or T terms
+             range, off by 2^-25 of the copy, whose largest value M lies in
+             [2^-6, 2^15) or is brought to [2^13, 2^14) (then 2^-38 of it is
+             that).  For W that is on sum_v |G_tv|.  h is copied times
+             64 s_t / s_max and meets G / s_t, with the kernel's s_t more than
+             half the one here: 2 s_max / 64 of it on sum_t |G_tv| / s_t (its
+             copy is scaled if 64 max |h| is below 2^-6, may be at or past 2^15).
+             Summed over k = V or T terms
              (k / 16 + 32) 2^-23; the outputs rounded by half a unit (2^-8 bf16,
              2^-24 fp32).
 """
@@ -71,13 +73,16 @@ class Bounds:
         return (k / 16 + 32 if self.bf16 else k / 2 + 32) * 2.0 ** -23
 
     def dh(self, G, s, out):
-        copy = 2.0 ** -25 * max(1.0, 2.0 ** -13 * np.abs(self.W).max()) * np.abs(G).sum(axis=1, keepdims=True)
+        most = np.abs(self.W).max()
+        copy = (2.0 ** -25 if 2.0 ** -6 <= most < 2.0 ** 15 else 2.0 ** -38 * most) * np.abs(G).sum(axis=1, keepdims=True)
         return (self._g(G, s) @ np.abs(self.W) + self._sum(G.shape[1]) * (np.abs(G) @ np.abs(self.W)) +
                 (copy if self.bf16 else 0.0) + half_step(out) * np.abs(G @ self.W))
 
     def dW(self, G, s, out):
         rows = (np.abs(G) / np.maximum(s, 1e-300)[:, None]).sum(axis=0)[:, None]
-        copy = 2 * s.max() * 2.0 ** -25 * max(2.0 ** -6, 2.0 ** -13 * np.abs(self.h).max()) * rows
+        most = 64 * np.abs(self.h).max()
+        step = 2.0 ** -38 * most if most < 2.0 ** -6 else max(2.0 ** -25, 2.0 ** -38 * most)
+        copy = 2 * s.max() / 64 * step * rows
         return (self._g(G, s).T @ np.abs(self.h) + self._sum(G.shape[0]) * (np.abs(G).T @ np.abs(self.h)) +
                 (copy if self.bf16 else 0.0) + half_step(out) * np.abs(G.T @ self.h))
 

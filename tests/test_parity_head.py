@@ -212,6 +212,21 @@ def test_one_gradient_alone_equals_both(T):
     assert torch.equal(topk_distill_bwd(*x, stats, want_dh=False, dW_dtype=BF)[1], dW)
 
 
+@pytest.mark.parametrize("T", [20, 140, 600])
+@pytest.mark.parametrize("shift", [-60, -18, 18, 60])
+def test_magnitudes_outside_fp16(T, shift):
+    """W times 2^shift and h times 2^-shift have the same logits; their fp16 copies need a scale of their own."""
+    _, h, W, y = make(T, 128, 900, BF, seed=4)
+    h, W = torch.ldexp(h.float(), torch.tensor(-shift)).to(BF), torch.ldexp(W.float(), torch.tensor(shift)).to(BF)
+    yg, hg, Wg = gpu(y, h, W)
+    tid = yg[:, None].repeat(1, 2)
+    z = torch.zeros(T, 2, device="cuda")
+    _, stats = topk_distill_fwd(yg, tid, z, hg, Wg, 0.5)
+    dh, dW = topk_distill_bwd(yg, tid, z, hg, Wg, stats, 0.5, 3.0)
+    r = oh.topk_distill(y, tid.cpu().numpy(), z.cpu().numpy(), h, W, 0.5, grad_scale=3.0)
+    check_grads(Bounds(h, W), r["G"], np.full(T, 3.0 / T), dh, dW)
+
+
 def test_views_of_fp32_rows():
     """fp32 rows of odd width start at any 4-byte boundary."""
     rng, h, W, y = make(40, 7, 90, F32, seed=8)
