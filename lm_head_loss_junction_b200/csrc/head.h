@@ -90,7 +90,7 @@ struct HeadFinish {
   int64_t all;                     // of the whole call (no result depends on the pieces)
   int64_t ldT;                     // row stride of the [*][T] outputs
   int n_splits;
-  const HeadPart* part;            // [T][n_splits]
+  const HeadPart* part;            // [T][n_splits], or NULL: from the logits (run_head_finish)
   float log2e;                     // of the logits
   const float* logits;             // [T][ld] or NULL
   int64_t ld;

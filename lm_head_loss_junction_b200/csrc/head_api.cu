@@ -124,7 +124,7 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
   f.all = p.T;
   f.ldT = p.T;
   f.n_splits = static_cast<int>(head_splits(p.V));
-  f.part = part;
+  f.part = p.bf16 || f.K > 0 ? part : nullptr;
   f.log2e = !p.bf16 ? mls::head_log2e(0, 1)
             : p.T <= mls::kFewTokens ? mls::head_log2e(p.D, mls::head_few_parts(mls::head_few_width(p.T)))
                                      : mls::head_log2e(p.D, 1);
@@ -154,7 +154,7 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
       w.picked = picked;
       err = p.T <= mls::kFewTokens ? mls::head_tc_few(p, w, st) : mls::head_tc_forward(p, w, st);
     } else {
-      err = mls::head_simt_logits(p, t0, n, logits, plan.ld, part, st);
+      err = mls::head_simt_logits(p, t0, n, logits, plan.ld, f.K > 0 ? part : nullptr, st);
     }
     if (err != cudaSuccess) return err;
     HeadFinish b = f;

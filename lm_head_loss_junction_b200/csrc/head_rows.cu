@@ -299,6 +299,40 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
   finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
 }
 
+// The same from the logits of a whole row (fp32 path without alternatives), one
+// block per token: one launch in place of the splits' statistics and their merge.
+__global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish f) {
+  __shared__ float sm[8], sz[8], su[8];
+  after_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x;
+  const float* row = f.logits + t * f.ld;
+  float top = -INFINITY;
+  for (int v = threadIdx.x; v < f.V; v += 256) top = fmaxf(top, __ldg(row + v));
+  top = warp_max(top);
+  if (lane == 0) sm[warp] = top;
+  __syncthreads();
+  top = warp_max(lane < 8 ? sm[lane] : -INFINITY);
+  const float m = top * f.log2e;
+  float z = 0.f, u = 0.f;
+  for (int v = threadIdx.x; v < f.V; v += 256) {
+    const float d = to_base2(__ldg(row + v), f.log2e, m), e = ex2(d);
+    z += e;
+    u = fmaf(d, e, u);
+  }
+  z = warp_sum(z);
+  u = warp_sum(u);
+  if (lane == 0) {
+    sz[warp] = z;
+    su[warp] = u;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  z = warp_sum(lane < 8 ? sz[lane] : 0.f);
+  u = warp_sum(lane < 8 ? su[lane] : 0.f);
+  finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+}
+
 // ------------------------------------------------------------------ top alternatives
 // One block per token.  The C = min(V, K + 4) largest logits by (value
 // descending, id ascending) lie in the C splits with the largest maxima by
@@ -791,6 +825,7 @@ cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bo
 }
 
 cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
+  if (f.part == nullptr) return head_launch(head_finish_rows_kernel, dim3(static_cast<unsigned>(f.T)), 256, 0, st, f);
   return head_launch(head_finish_kernel, dim3(static_cast<unsigned>((f.T + 7) / 8)), 256, 0, st, f);
 }
 
