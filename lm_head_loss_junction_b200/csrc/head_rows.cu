@@ -836,15 +836,20 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const int list = padded < 1024 ? static_cast<int>(padded) : 1024;
   const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t) +
                       static_cast<size_t>(f.n_splits) * 8;
-  // Few tokens leave SMs idle: their blocks get all the warps that help (T = 1, D = 2304, K = 8: 24 us with 256
-  // threads, 15 with 1024).
-  const bool wide = f.all <= 148;
+  // Few tokens leave SMs idle: their blocks get the warps that help, one per product (T = 1, D = 2304, K = 8: the whole
+  // call 50.2 us with 512 threads, 51.4 with 1024; T = 24, D = 1024, K = 20: 34.6 and 32.6).
   // Of many tokens small blocks are best, more of them in flight per SM, until the products outweigh the steps before
   // them (T = 4096, K = 32, with 128 and 256 threads: D = 64 103 and 120 us, 512 114 and 127, 2304 285 and 266).
-  const bool light = static_cast<int64_t>(C + f.N) * f.D <= 40000;
-  auto fn = f.bf16 ? (wide ? head_top_kernel<true, 1024> : light ? head_top_kernel<true, 128> : head_top_kernel<true, 256>)
-                   : (wide ? head_top_kernel<false, 1024> : head_top_kernel<false, 128>);
-  const unsigned threads = wide ? 1024 : light || !f.bf16 ? 128 : 256;
+  const bool few = f.all <= 148, short_list = C + f.N <= 16;
+  const bool light = static_cast<int64_t>(C + f.N) * f.D <= 40000 || !f.bf16;
+  const unsigned threads = few ? (short_list ? 512 : 1024) : light ? 128 : 256;
+  auto fn = f.bf16 ? (threads == 1024  ? head_top_kernel<true, 1024>
+                      : threads == 512 ? head_top_kernel<true, 512>
+                      : threads == 256 ? head_top_kernel<true, 256>
+                                       : head_top_kernel<true, 128>)
+                   : (threads == 1024  ? head_top_kernel<false, 1024>
+                      : threads == 512 ? head_top_kernel<false, 512>
+                                       : head_top_kernel<false, 128>);
   // the limit is the same on every call: another host thread's call may set it between here and the launch
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmemLimit);
   if (err != cudaSuccess) return err;
