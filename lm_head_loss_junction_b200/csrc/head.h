@@ -57,6 +57,8 @@ struct HeadProblem {
 struct HeadEntriesIn {
   int64_t T, V;
   int N;
+  const void* h;                   // bf16 backward: [T][D], for its rows' largest magnitudes
+  int64_t D;
   const int32_t* ids;              // [T][N]; -1: absent
   // log probabilities, backward
   const float* stats;              // [2][T]: lse, entropy (distillation: row 0 of [3][T])
@@ -75,14 +77,33 @@ struct HeadEntries {
   int2* e;                         // [T][Ntot] (id, position or coefficient bits)
   uint8_t* first;                  // [splits + 1][T]
   float4* row;                     // [T] (lse, A, B, s); backward only
-  unsigned int* smax;              // backward only: largest s as float bits, [1] and [2] the largest magnitudes of
-                                   // the fp16 copies of W and h (all three set to 0 with the entries)
+  unsigned int* smax;              // backward only, as float bits, set to 0 with the entries: [0] a bound on s_t |h_ti|
+                                   // (a power of two), [1] the largest magnitude of the chunk of W
   int Ntot;
 };
 size_t head_entries_bytes(int64_t T, int64_t V, int Ntot, bool backward);
 HeadEntries head_entries_layout(int64_t T, int64_t V, int Ntot, bool backward, void* ws);
+
+// fp16 copies of bf16 operands for the gradient products (head_copy.cuh).
+struct HeadCopyW {
+  const void* src;
+  __half* dst;
+  int64_t n_vec;                   // vectors of 8 values; 0: nothing to do
+  unsigned int* maxbits;
+  float* inv;                      // 1 / the copy's scale
+};
+struct HeadCopyH {
+  const void* src;
+  __half* dst;
+  int64_t n_vec;
+  int vec_per_row;
+  const float4* row;
+  const unsigned int* smax;
+};
+
+// w (may be NULL): a copy of W made by further blocks of the same launch.
 cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bool backward, int32_t* status,
-                             cudaStream_t st);
+                             const HeadCopyW* w, cudaStream_t st);
 
 // ------------------------------------------------------------------ per-token results
 struct HeadFinish {
@@ -113,6 +134,7 @@ struct HeadFinish {
   const float* weights;
   float alpha;
   float* terms;                    // [3][ldT]
+  float* losses;                   // [3] means of the terms, or NULL: left to the caller (run_head_finish)
   int32_t* status;
 };
 cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st);      // lse, entropy, picks or loss terms
@@ -139,11 +161,12 @@ inline int head_few_width(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <=
 constexpr int head_few_parts(int width) { return width <= 32 ? 8 : 256 / width; }
 cudaError_t head_tc_few(const HeadProblem& p, const HeadForward& f, cudaStream_t st);
 
-// dh and dW (either may be NULL) from the entries, one chunk of the vocabulary at a time.
+// dh and dW (either may be NULL) from the entries, which it makes first, one
+// chunk of the vocabulary at a time.
 size_t head_tc_bwd_bytes(const HeadProblem& p, int64_t Vc);
 int64_t head_tc_bwd_chunk(const HeadProblem& p, size_t budget);
-cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* dh, void* dW, bool dW_bf16,
-                             int accumulate, void* ws, int64_t Vc, cudaStream_t st);
+cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntriesIn& in, const HeadEntries& en, void* dh, void* dW,
+                             bool dW_bf16, int accumulate, void* ws, int64_t Vc, cudaStream_t st);
 
 // ------------------------------------------------------------------ CUDA-core path (fp32)
 cudaError_t head_simt_logits(const HeadProblem& p, int64_t t0, int64_t Tb, float* logits, int64_t ld,

@@ -108,7 +108,7 @@ cudaError_t forward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, Hea
   HeadEntries en{};
   if (!plan.store) {
     en = mls::head_entries_layout(p.T, p.V, Ntot, false, q);
-    err = mls::run_head_entries(in, en, false, p.status, st);
+    err = mls::run_head_entries(in, en, false, p.status, nullptr, st);
     if (err != cudaSuccess) return err;
   }
   q += plan.entries;
@@ -200,18 +200,20 @@ size_t backward_bytes(const HeadProblem& p, int Ntot) {
   return e + mls::head_tc_bwd_bytes(p, Vc);
 }
 
-mls_status backward(const HeadProblem& p, const HeadEntriesIn& in, int Ntot, void* dh, void* dW, bool dW_bf16,
+mls_status backward(const HeadProblem& p, HeadEntriesIn in, int Ntot, void* dh, void* dW, bool dW_bf16,
                     int accumulate, void* ws, size_t ws_bytes, cudaStream_t st) {
   const size_t e = mls::head_entries_bytes(p.T, p.V, Ntot, true);
   const HeadEntries en = mls::head_entries_layout(p.T, p.V, Ntot, true, ws);
   char* rest = static_cast<char*>(ws) + e;
-  cudaError_t err = mls::run_head_entries(in, en, true, p.status, st);
-  if (err != cudaSuccess) return MLS_ERR_CUDA;
   if (p.bf16) {
+    in.h = p.h;
+    in.D = p.D;
     const int64_t Vc = mls::head_tc_bwd_chunk(p, ws_bytes - e);
     if (Vc <= 0) return MLS_ERR_WORKSPACE;
-    return from_cuda(mls::head_tc_backward(p, en, dh, dW, dW_bf16, accumulate, rest, Vc, st));
+    return from_cuda(mls::head_tc_backward(p, in, en, dh, dW, dW_bf16, accumulate, rest, Vc, st));
   }
+  const cudaError_t err = mls::run_head_entries(in, en, true, p.status, nullptr, st);
+  if (err != cudaSuccess) return MLS_ERR_CUDA;
   return from_cuda(mls::head_simt_backward(p, en, static_cast<float*>(dh), static_cast<float*>(dW), accumulate,
                                            reinterpret_cast<float*>(rest), simt_block(p, ws_bytes - e), st));
 }
@@ -391,7 +393,12 @@ mls_status mls_topk_distill_fwd(int64_t T, int64_t D, int64_t V, int K, const in
   f.alpha = alpha_d;
   const ForwardPlan plan = forward_fit(p, K + 1, 0, true, ws_bytes);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // as few tokens as a block has warps: one block finishes them and their means (90 tokens in one block took 4 us
+  // more than two launches)
+  const bool one = p.bf16 && T <= 32;
+  f.losses = one ? losses : nullptr;
   MLS_TRY(from_cuda(forward(p, in, K + 1, f, plan, workspace, st)));
+  if (one) return MLS_OK;
   const float* terms = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.entries);
   return from_cuda(mls::launch_row_means(terms, 3, T, losses, st));
 }

@@ -18,6 +18,12 @@ bool head_make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t ou
 // SMs of the current device.
 int head_num_sms();
 
+// Blocks of 256 threads for a copy of n_vec vectors.
+inline unsigned head_copy_blocks(int64_t n_vec) {
+  const int64_t want = (n_vec + 2047) / 2048, cap = 8 * static_cast<int64_t>(head_num_sms());
+  return static_cast<unsigned>(want < 1 ? 1 : want < cap ? want : cap);
+}
+
 // Launches a kernel that calls after_previous() (head_dev.cuh) before it touches
 // global memory: it may be set up while the one before it on the stream ends.
 // A step of a few tokens is ten launches of a few microseconds each, of which

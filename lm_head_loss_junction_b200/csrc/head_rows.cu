@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "head.h"
+#include "head_copy.cuh"
 #include "head_dev.cuh"
 #include "head_host.h"
 
@@ -39,10 +40,17 @@ __device__ __forceinline__ float pow2_of(float m) {
   return ldexpf(1.f, e);
 }
 
+// Blocks past the tokens' make the fp16 copy of W that dh will read.
 __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn in, const HeadEntries out,
-                                                           bool backward, int n_splits, int32_t* status) {
+                                                           bool backward, int n_splits, unsigned token_blocks,
+                                                           const HeadCopyW w_copy, int32_t* status) {
   __shared__ __align__(16) EntrySmem s;
   after_previous();
+  if (blockIdx.x >= token_blocks) {
+    copy_w(w_copy, static_cast<int64_t>(blockIdx.x - token_blocks) * 256 + threadIdx.x,
+           static_cast<int64_t>(gridDim.x - token_blocks) * 256);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kEntryTokens;
   const int N = in.N, tot = out.Ntot;
@@ -53,6 +61,16 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
     float c[kPerLane];
     bool there[kPerLane];
     bool bad = false;
+    float h_most = 0.f;
+    if (backward && in.h != nullptr) {
+      const uint4* row = static_cast<const uint4*>(in.h) + t * (in.D / 8);
+      for (int64_t j = lane; j < in.D / 8; j += 32) {
+        float x[8];
+        bf16x8_to_f32(__ldg(row + j), x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h_most = fmaxf(h_most, fabsf(x[k]));
+      }
+    }
     const float w = in.weights != nullptr ? in.weights[t] : 1.f;
     const int32_t y = in.y != nullptr ? in.y[t] : 0;
     // a token with a bad target is left out; one of weight 0 has no gradient, but terms of its own in stats
@@ -117,7 +135,15 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
       if (lane == 0) {
         const float r = scale != 0.f ? 1.f / scale : 0.f;
         out.row[t] = make_float4(in.stats[t], A * r, B * r, scale);
-        if (scale > 0.f) atomicMax(out.smax, __float_as_uint(scale));
+      }
+      if (in.h != nullptr) {
+        // a power of two above s |h| (a row of zeros, or of nothing that is a number, counts as 1)
+        h_most = warp_max(h_most);
+        if (lane == 0 && scale > 0.f) {
+          int e = ilogbf(scale) + (h_most > 0.f && h_most <= 3.4e38f ? ilogbf(h_most) + 1 : 0);
+          e = e < -126 ? -126 : (e > 126 ? 126 : e);
+          atomicMax(out.smax, __float_as_uint(ldexpf(1.f, e)));
+        }
       }
     }
     if (__any_sync(kFull, bad) && lane == 0) set_flag(status, MLS_DEVFLAG_BAD_ID);
@@ -297,6 +323,30 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
   }
   warp_merge(m, z, u);
   finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+}
+
+// The same for the few tokens of one block, and the means of their loss terms:
+// one launch in place of two.
+
+__global__ void __launch_bounds__(1024) head_finish_loss_kernel(const HeadFinish f) {
+  after_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t t = warp; t < f.T; t += 32) {
+    float m = -INFINITY, z = 0.f, u = 0.f;
+    for (int s = lane; s < f.n_splits; s += 32) {
+      const HeadPart p = __ldg(f.part + t * f.n_splits + s);
+      merge_part(m, z, u, p.x, p.y, p.z);
+    }
+    warp_merge(m, z, u);
+    finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+  }
+  __syncthreads();
+  if (warp < 3) {
+    float sum = 0.f;
+    for (int64_t t = lane; t < f.T; t += 32) sum += f.terms[warp * f.ldT + t];
+    sum = warp_sum(sum);
+    if (lane == 0) f.losses[warp] = sum / static_cast<float>(f.T);
+  }
 }
 
 // The same from the logits of a whole row (fp32 path without alternatives), one
@@ -814,17 +864,19 @@ HeadEntries head_entries_layout(int64_t T, int64_t V, int Ntot, bool backward, v
 }
 
 cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bool backward, int32_t* status,
-                             cudaStream_t st) {
+                             const HeadCopyW* w, cudaStream_t st) {
   if (backward) {
-    const cudaError_t err = cudaMemsetAsync(out.smax, 0, 3 * sizeof(unsigned int), st);
+    const cudaError_t err = cudaMemsetAsync(out.smax, 0, 2 * sizeof(unsigned int), st);
     if (err != cudaSuccess) return err;
   }
   const unsigned grid = static_cast<unsigned>((in.T + kEntryTokens - 1) / kEntryTokens);
-  return head_launch(head_entries_kernel, dim3(grid), 256, 0, st, in, out, backward,
-                     static_cast<int>(head_splits(in.V)), status);
+  const unsigned more = w != nullptr ? head_copy_blocks(w->n_vec) : 0;
+  return head_launch(head_entries_kernel, dim3(grid + more), 256, 0, st, in, out, backward,
+                     static_cast<int>(head_splits(in.V)), grid, w != nullptr ? *w : HeadCopyW{}, status);
 }
 
 cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
+  if (f.losses != nullptr) return head_launch(head_finish_loss_kernel, dim3(1), 1024, 0, st, f);
   if (f.part == nullptr) return head_launch(head_finish_rows_kernel, dim3(static_cast<unsigned>(f.T)), 256, 0, st, f);
   return head_launch(head_finish_kernel, dim3(static_cast<unsigned>((f.T + 7) / 8)), 256, 0, st, f);
 }

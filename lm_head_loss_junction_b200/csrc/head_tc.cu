@@ -27,6 +27,7 @@
 #include <mutex>
 
 #include "head.h"
+#include "head_copy.cuh"
 #include "head_dev.cuh"
 #include "head_host.h"
 #include "umma.cuh"
@@ -50,96 +51,16 @@ constexpr float kMasked = -1.0e38f;      // logit of a column past V: finite to 
 
 enum Epi { kStats, kLogits, kGrad, kDh, kDw };
 
-// ------------------------------------------------------------------ fp16 operand copies
-// dst[r][:] = fp16(src[r][:] * f_r), f_r = 1, or 64 times the row's scale over
-// the largest one (64: rows down to 2^-20 of the largest scale stay in fp16's
-// normal range at values near 1, values up to 512 do not pass it); tracks the largest magnitude.  kind::f16 takes A and B of one
-// type, so G' in fp16 needs W and h in fp16.  bf16's 8 significant bits fit in
-// fp16's 11: values in its normal range convert exactly.
-struct CopyArgs {
-  const uint4* src;
-  uint4* dst;
-  int64_t n_vec;
-  int vec_per_row;
-  const float4* row;               // row scales in .w (NULL: 1)
-  const unsigned int* smax;
-  unsigned int* maxbits;
-  float* inv;
-};
-
-__device__ __forceinline__ uint4 to_half8(const uint4& v, float f, float& mx) {
-  float x[8];
-  bf16x8_to_f32(v, x);
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    // a row of scale 0 is left out, whatever it holds
-    const float lo = f == 0.f ? 0.f : x[2 * k] * f, hi = f == 0.f ? 0.f : x[2 * k + 1] * f;
-    mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
-    __half2 h = __floats2half2_rn(lo, hi);
-    w[k] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-constexpr float kRowLift = 64.f;
-
-__device__ __forceinline__ float copy_factor(const CopyArgs& a, int64_t i, float smax) {
-  if (a.row == nullptr) return 1.f;
-  return smax > 0.f ? a.row[i / a.vec_per_row].w / smax * kRowLift : 0.f;
-}
-
-// Thread `first` of `stride` threads.
-__device__ __forceinline__ void copy_part(const CopyArgs& a, int64_t first, int64_t stride) {
-  if (a.n_vec == 0) return;
-  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
-  float mx = 0.f;
-  int64_t i = first;
-  for (; i + 7 * stride < a.n_vec; i += 8 * stride) {
-    uint4 v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __ldg(a.src + i + k * stride);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) a.dst[i + k * stride] = to_half8(v[k], copy_factor(a, i + k * stride, smax), mx);
-  }
-  for (; i < a.n_vec; i += stride) a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax), mx);
-  mx = warp_max(mx);
-  if ((threadIdx.x & 31) == 0 && mx > 0.f) atomicMax(a.maxbits, __float_as_uint(mx));
-}
-
-struct CopyJobs {
-  CopyArgs w, h;
-};
-
-__global__ void __launch_bounds__(256) head_copy_kernel(const CopyJobs jobs) {
+// W's copy in a kernel of its own (later chunks of few tokens), and its scale.
+__global__ void __launch_bounds__(256) head_copy_kernel(const HeadCopyW w) {
   after_previous();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  copy_part(blockIdx.y == 0 ? jobs.w : jobs.h, first, static_cast<int64_t>(gridDim.x) * blockDim.x);
+  copy_w(w, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
-// The copy again with a power-of-two scale when the largest magnitude is at or
-// past 2^15 or below 2^-6; the reciprocal of the scale for the epilogue.
-__device__ __forceinline__ void rescale_part(const CopyArgs& a, int64_t first, int64_t stride) {
-  if (a.n_vec == 0) return;
-  const float mx = __uint_as_float(*a.maxbits);
-  float s = 1.f;
-  if (mx <= 3.4e38f && (mx >= 32768.f || (mx > 0.f && mx < 1.f / 64.f))) {
-    int e = 13 - ilogbf(mx);
-    e = e < -126 ? -126 : (e > 126 ? 126 : e);
-    s = ldexpf(1.f, e);
-  }
-  if (first == 0) *a.inv = 1.f / (a.row != nullptr ? s * kRowLift : s);
-  if (s == 1.f) return;
-  const float smax = a.row != nullptr ? __uint_as_float(*a.smax) : 1.f;
-  float unused = 0.f;
-  for (int64_t i = first; i < a.n_vec; i += stride)
-    a.dst[i] = to_half8(__ldg(a.src + i), copy_factor(a, i, smax) * s, unused);
-}
-
-__global__ void __launch_bounds__(256) head_rescale_kernel(const CopyJobs jobs) {
+__global__ void __launch_bounds__(256) head_rescale_kernel(const HeadCopyW w) {
   after_previous();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  rescale_part(blockIdx.y == 0 ? jobs.w : jobs.h, first, static_cast<int64_t>(gridDim.x) * blockDim.x);
+  rescale_w(w, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+            static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 struct TileMaps {
@@ -171,10 +92,11 @@ struct TileArgs {
   void* out;
   float* acc;                      // dh partial sums of earlier chunks [rows][cols] (NULL: none)
   int accumulate;
-  const float* inv;                // device: 1 / scale of the fp16 copy
-  const unsigned int* smax;        // device: largest row scale (dw)
-  CopyJobs copy;                   // grad: fp16 copies made by two more warps,
-  int copied;                      // or made already and given their scale by them
+  const float* inv;                // dh, device: 1 / scale of the fp16 copy of W
+  const unsigned int* smax;        // dw, device: the bound that scales the copy of h
+  HeadCopyW copy_w;                // grad: fp16 copies made by two more warps
+  HeadCopyH copy_h;
+  int w_copied;                    // W's copy is made already, they give it its scale
   int32_t* status;
 };
 
@@ -433,9 +355,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       __syncwarp();
     }
   } else {
-    const float inv = __ldg(a.inv);
-    float alpha = inv;
-    if constexpr (EPI == kDw) alpha = inv * __uint_as_float(__ldg(a.smax));
+    const float alpha = EPI == kDw ? __uint_as_float(__ldg(a.smax)) / kRowLift : __ldg(a.inv);
     const float rs = EPI == kDh && valid ? __ldg(&a.row[row].w) : 1.f;
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
@@ -644,13 +564,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
     // ---------------------------------------------------------------- fp16 copies for dh and dw
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x - kThreads;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kCopyThreads;
-    if (a.copied) {
-      rescale_part(a.copy.w, first, stride);
-      rescale_part(a.copy.h, first, stride);
-    } else {
-      copy_part(a.copy.w, first, stride);
-      copy_part(a.copy.h, first, stride);
-    }
+    if (a.w_copied) rescale_w(a.copy_w, first, stride);
+    else if (a.copy_w.n_vec > 0) copy_w(a.copy_w, first, stride);
+    copy_h(a.copy_h, first, stride);
   }
 
   __syncthreads();
@@ -844,26 +760,6 @@ int dh_parts(int64_t T, int64_t D, int64_t V) {
   return best;
 }
 
-void set_copy(CopyArgs& a, const void* src, __half* dst, int64_t rows, int64_t D, const HeadEntries* scaled,
-              unsigned int* maxbits, float* inv) {
-  a.src = static_cast<const uint4*>(src);
-  a.dst = reinterpret_cast<uint4*>(dst);
-  a.n_vec = rows * D / 8;
-  a.vec_per_row = static_cast<int>(D / 8);
-  if (scaled != nullptr) {
-    a.row = scaled->row;
-    a.smax = scaled->smax;
-  }
-  a.maxbits = maxbits;
-  a.inv = inv;
-}
-
-dim3 copy_grid(const CopyJobs& j) {
-  const int64_t n = j.w.n_vec > j.h.n_vec ? j.w.n_vec : j.h.n_vec;
-  const int64_t want = (n + 1023) / 1024, cap = 8 * static_cast<int64_t>(head_num_sms());
-  return dim3(static_cast<unsigned>(want < cap ? want : cap), 2);
-}
-
 // Backward workspace: [G' chunk: T x round_up(Vc, 64) f16][dh partial sums:
 // T x D f32, only with more than one chunk][parts of dh: T x D f32 each][h in
 // fp16][the chunk's W rows in fp16][copy scales].
@@ -883,7 +779,7 @@ BwdWs bwd_layout(const HeadProblem& p, int64_t Vc) {
   w.part = w.parts > 1 ? head_align(static_cast<size_t>(w.parts) * p.T * p.D * 4) : 0;
   w.h16 = head_align(static_cast<size_t>(p.T) * p.D * 2);
   w.w16 = head_align(static_cast<size_t>(Vc) * p.D * 2);
-  w.aux = 256;
+  w.aux = 256;                       // W's copy scale
   return w;
 }
 
@@ -928,8 +824,8 @@ int64_t head_tc_bwd_chunk(const HeadProblem& p, size_t budget) {
   return even < lo * kBN ? even : lo * kBN;
 }
 
-cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* dh, void* dW, bool dW_bf16,
-                             int accumulate, void* ws, int64_t Vc, cudaStream_t st) {
+cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntriesIn& in, const HeadEntries& en, void* dh, void* dW,
+                             bool dW_bf16, int accumulate, void* ws, int64_t Vc, cudaStream_t st) {
   const BwdWs w = bwd_layout(p, Vc);
   char* q = static_cast<char*>(ws);
   __half* G = reinterpret_cast<__half*>(q);
@@ -942,29 +838,29 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
   q += w.h16;
   __half* w16 = reinterpret_cast<__half*>(q);
   q += w.w16;
-  unsigned int* maxbits = en.smax + 1;               // [0] W, [1] h; 0 from the entries' launch
   float* inv = reinterpret_cast<float*>(q);
   cudaError_t err = cudaSuccess;
-  // From 512 tokens on the tensor pipe bounds the G' kernel and two more warps of it make the fp16 copies beside it;
-  // below, reading W bounds it and the copies, in so few threads, would prolong it.  Whole steps, V = 32771, D = 1024,
-  // copies beside it and before it in a kernel of their own: T = 300 215 and 201 us, 777 265 and 278, 1200 329 and
-  // 354, 2047 530 and 535.
+  // From 512 tokens on the tensor pipe bounds the G' kernel and two more warps of it copy W beside it; below, reading W
+  // bounds it and the copy, in so few threads, would prolong it: further blocks of the entries' launch make it.  Whole
+  // steps, V = 32771, D = 1024, beside and before: T = 300 215 and 201 us, 777 265 and 278, 1200 329 and 354, 2047 530
+  // and 535.
   const bool beside = p.T >= 512;
   for (int64_t v0 = 0; v0 < p.V; v0 += Vc) {
     const int64_t n = v0 + Vc <= p.V ? Vc : p.V - v0;
     const bool first = v0 == 0, last = v0 + n >= p.V;
     const void* Wc = static_cast<const __nv_bfloat16*>(p.W) + v0 * p.D;
-    CopyJobs copy{};
-    if (dh != nullptr) set_copy(copy.w, Wc, w16, n, p.D, nullptr, maxbits, inv);
-    if (dW != nullptr && first) set_copy(copy.h, p.h, h16, p.T, p.D, &en, maxbits + 1, inv + 1);
-    const bool any = copy.w.n_vec > 0 || copy.h.n_vec > 0;
-    if (any && !first) {
-      err = cudaMemsetAsync(maxbits, 0, sizeof(unsigned int), st);
+    HeadCopyW w_copy{};
+    if (dh != nullptr) w_copy = HeadCopyW{Wc, w16, n * p.D / 8, en.smax + 1, inv};
+    if (first) {
+      err = run_head_entries(in, en, true, p.status, beside || dh == nullptr ? nullptr : &w_copy, st);
       if (err != cudaSuccess) return err;
-    }
-    if (any && !beside) {
-      err = head_launch(head_copy_kernel, copy_grid(copy), 256, 0, st, copy);
+    } else if (dh != nullptr) {
+      err = cudaMemsetAsync(en.smax + 1, 0, sizeof(unsigned int), st);
       if (err != cudaSuccess) return err;
+      if (!beside) {
+        err = head_launch(head_copy_kernel, dim3(head_copy_blocks(w_copy.n_vec)), 256, 0, st, w_copy);
+        if (err != cudaSuccess) return err;
+      }
     }
     TileMaps maps;
     TileArgs a{};
@@ -984,12 +880,14 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
     a.G = G;
     a.ld = w.ldg;
     a.gcols = static_cast<int>((n + 63) / 64 * 64);
-    a.copy = copy;
-    a.copied = beside ? 0 : 1;
+    a.copy_w = w_copy;
+    a.w_copied = beside ? 0 : 1;
+    if (dW != nullptr && first)
+      a.copy_h = HeadCopyH{p.h, h16, p.T * p.D / 8, static_cast<int>(p.D / 8), en.row, en.smax};
     err = run_tiles<kGrad, false>(maps, a, p.D, 1, st);
     if (err != cudaSuccess) return err;
-    if (any && beside) {
-      err = head_launch(head_rescale_kernel, copy_grid(copy), 256, 0, st, copy);
+    if (dh != nullptr && beside) {
+      err = head_launch(head_rescale_kernel, dim3(head_copy_blocks(w_copy.n_vec)), 256, 0, st, w_copy);
       if (err != cudaSuccess) return err;
     }
     if (dh != nullptr) {
@@ -1033,7 +931,6 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntries& en, void* 
       d.status = p.status;
       d.rows = static_cast<int>(n);
       d.cols = static_cast<int>(p.D);
-      d.inv = inv + 1;
       d.smax = en.smax;
       d.accumulate = accumulate;
       if (!head_make_map(&maps.a, G, a.gcols, p.T, w.ldg, 64, kBK, true)) return cudaErrorInvalidValue;

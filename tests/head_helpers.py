@@ -21,9 +21,9 @@ of a partial sum each; a partial sum is at most sum_i |h_i w_i|):
              range, off by 2^-25 of the copy, whose largest value M lies in
              [2^-6, 2^15) or is brought to [2^13, 2^14) (then 2^-38 of it is
              that).  For W that is on sum_v |G_tv|.  h is copied times
-             64 s_t / s_max and meets G / s_t, with the kernel's s_t more than
-             half the one here: 2 s_max / 64 of it on sum_t |G_tv| / s_t (its
-             copy is scaled if 64 max |h| is below 2^-6, may be at or past 2^15).
+             2^14 s_t / b, with b at most twice the largest s_t |h_ti|, and meets
+             G / s_t, with the kernel's s_t more than half the one here:
+             2 2^-39 2 s_max max |h| on sum_t |G_tv| / s_t.
              Summed over k = V or T terms
              (k / 16 + 32) 2^-23; the outputs rounded by half a unit (2^-8 bf16,
              2^-24 fp32).
@@ -80,9 +80,7 @@ class Bounds:
 
     def dW(self, G, s, out):
         rows = (np.abs(G) / np.maximum(s, 1e-300)[:, None]).sum(axis=0)[:, None]
-        most = 64 * np.abs(self.h).max()
-        step = 2.0 ** -38 * most if most < 2.0 ** -6 else max(2.0 ** -25, 2.0 ** -38 * most)
-        copy = 2 * s.max() / 64 * step * rows
+        copy = 2 * 2.0 ** -39 * 2 * s.max() * np.abs(self.h).max() * rows
         return (self._g(G, s).T @ np.abs(self.h) + self._sum(G.shape[0]) * (np.abs(G).T @ np.abs(self.h)) +
                 (copy if self.bf16 else 0.0) + half_step(out) * np.abs(G.T @ self.h))
 
