@@ -37,11 +37,11 @@ __device__ __forceinline__ void copy_w(const HeadCopyW& a, int64_t first, int64_
   for (; i + 7 * stride < a.n_vec; i += 8 * stride) {
     uint4 v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __ldg(src + i + k * stride);
+    for (int k = 0; k < 8; ++k) v[k] = src[i + k * stride];
 #pragma unroll
     for (int k = 0; k < 8; ++k) dst[i + k * stride] = to_half8(v[k], 1.f, mx);
   }
-  for (; i < a.n_vec; i += stride) dst[i] = to_half8(__ldg(src + i), 1.f, mx);
+  for (; i < a.n_vec; i += stride) dst[i] = to_half8(src[i], 1.f, mx);
   mx = warp_max(mx);
   if ((threadIdx.x & 31) == 0 && mx > 0.f) atomicMax(a.maxbits, __float_as_uint(mx));
 }
@@ -61,7 +61,7 @@ __device__ __forceinline__ void rescale_w(const HeadCopyW& a, int64_t first, int
   if (s == 1.f) return;
   float unused = 0.f;
   for (int64_t i = first; i < a.n_vec; i += stride)
-    reinterpret_cast<uint4*>(a.dst)[i] = to_half8(__ldg(static_cast<const uint4*>(a.src) + i), s, unused);
+    reinterpret_cast<uint4*>(a.dst)[i] = to_half8(static_cast<const uint4*>(a.src)[i], s, unused);
 }
 
 __device__ __forceinline__ void copy_h(const HeadCopyH& a, int64_t first, int64_t stride) {
@@ -79,13 +79,13 @@ __device__ __forceinline__ void copy_h(const HeadCopyH& a, int64_t first, int64_
     float f[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[k] = __ldg(src + i + k * stride);
+      v[k] = src[i + k * stride];
       f[k] = factor(i + k * stride);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) dst[i + k * stride] = to_half8(v[k], f[k], unused);
   }
-  for (; i < a.n_vec; i += stride) dst[i] = to_half8(__ldg(src + i), factor(i), unused);
+  for (; i < a.n_vec; i += stride) dst[i] = to_half8(src[i], factor(i), unused);
 }
 
 }  // namespace mls

@@ -19,7 +19,9 @@ __device__ __forceinline__ float to_base2(float l, float log2e, float m) { retur
 
 // The kernels of one call are launched so that the next may be set up while one
 // runs; each thread waits here, before its first access to global memory, until
-// everything before on the stream is complete and visible.
+// everything before on the stream is complete and visible.  Loads after it are
+// plain ones: a read-only load (__ldg, or of a const __restrict__ pointer) may
+// be moved before the wait, where the kernel before still writes.
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

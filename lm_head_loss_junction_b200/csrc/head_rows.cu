@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
       const uint4* row = static_cast<const uint4*>(in.h) + t * (in.D / 8);
       for (int64_t j = lane; j < in.D / 8; j += 32) {
         float x[8];
-        bf16x8_to_f32(__ldg(row + j), x);
+        bf16x8_to_f32(row[j], x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h_most = fmaxf(h_most, fabsf(x[k]));
       }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
   if (t >= f.T) return;
   float m = -INFINITY, z = 0.f, u = 0.f;
   for (int s = lane; s < f.n_splits; s += 32) {
-    const HeadPart p = __ldg(f.part + t * f.n_splits + s);
+    const HeadPart p = f.part[t * f.n_splits + s];
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(1024) head_finish_loss_kernel(const HeadFinish
   for (int64_t t = warp; t < f.T; t += 32) {
     float m = -INFINITY, z = 0.f, u = 0.f;
     for (int s = lane; s < f.n_splits; s += 32) {
-      const HeadPart p = __ldg(f.part + t * f.n_splits + s);
+      const HeadPart p = f.part[t * f.n_splits + s];
       merge_part(m, z, u, p.x, p.y, p.z);
     }
     warp_merge(m, z, u);
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
   const int64_t t = blockIdx.x;
   const float* row = f.logits + t * f.ld;
   float top = -INFINITY;
-  for (int v = threadIdx.x; v < f.V; v += 256) top = fmaxf(top, __ldg(row + v));
+  for (int v = threadIdx.x; v < f.V; v += 256) top = fmaxf(top, row[v]);
   top = warp_max(top);
   if (lane == 0) sm[warp] = top;
   __syncthreads();
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
   const float m = top * f.log2e;
   float z = 0.f, u = 0.f;
   for (int v = threadIdx.x; v < f.V; v += 256) {
-    const float d = to_base2(__ldg(row + v), f.log2e, m), e = ex2(d);
+    const float d = to_base2(row[v], f.log2e, m), e = ex2(d);
     z += e;
     u = fmaf(d, e, u);
   }
@@ -498,9 +498,9 @@ __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, 
     for (int i = lane; i < n; i += 32) {
       uint4 w[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) w[g] = __ldg(b[g] + i);
+      for (int g = 0; g < G; ++g) w[g] = b[g][i];
       float x[8];
-      bf16x8_to_f32(__ldg(a + i), x);
+      bf16x8_to_f32(a[i], x);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float y[8];
@@ -512,9 +512,9 @@ __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, 
   } else {
     const float* a = static_cast<const float*>(h);
     for (int64_t i = lane; i < D; i += 32) {
-      const double x = __ldg(a + i);
+      const double x = a[i];
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = fma(x, static_cast<double>(__ldg(static_cast<const float*>(W) + id[g] * D + i)), acc[g]);
+      for (int g = 0; g < G; ++g) acc[g] = fma(x, static_cast<double>(static_cast<const float*>(W)[id[g] * D + i]), acc[g]);
     }
   }
 #pragma unroll
@@ -540,9 +540,9 @@ __device__ __forceinline__ void dots_fast(const void* h, const void* W, int64_t 
   for (int i = lane; i < n; i += 32) {
     uint4 w[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) w[g] = __ldg(b[g] + i);
+    for (int g = 0; g < G; ++g) w[g] = b[g][i];
     float x[8];
-    bf16x8_to_f32(__ldg(a + i), x);
+    bf16x8_to_f32(a[i], x);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float y[8], p = 0.f;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   // the statistics, and the largest logit
   float m = -INFINITY, z = 0.f, u = 0.f, largest = -INFINITY;
   for (int i = threadIdx.x; i < n_splits; i += kTopThreads) {
-    const HeadPart p = __ldg(f.part + t * n_splits + i);
+    const HeadPart p = f.part[t * n_splits + i];
     maxima[i] = p.w;
     largest = fmaxf(largest, p.w);
     merge_part(m, z, u, p.x, p.y, p.z);
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   if (n_splits >= C) {
     for (int i = threadIdx.x; i < n_splits; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, maxima[i])], 1);
   } else {
-    for (int i = threadIdx.x; i < f.V; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, __ldg(row + i))], 1);
+    for (int i = threadIdx.x; i < f.V; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, row[i])], 1);
   }
   __syncthreads();
   if (warp == 0) {
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   for (int i = warp; i < n_take; i += kWarps) {
     const int col = sel[i] * kHeadSplit + lane * 4;
     if (col >= f.V) continue;                            // rows are padded to a multiple of 64
-    const float4 v4 = __ldg(reinterpret_cast<const float4*>(row + col));
+    const float4 v4 = *reinterpret_cast<const float4*>(row + col);
     const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   int n = s.count;
   if (n > list) {
     // keys made from the logits on every pass; C of them are at or above the C-th
-    const auto at = [&](int i) { return top_key(__ldg(row + i), static_cast<uint32_t>(i)); };
+    const auto at = [&](int i) { return top_key(row[i], static_cast<uint32_t>(i)); };
     const uint64_t last = select_kth<kTopThreads>(at, static_cast<int>(f.V), C, s.hist, s.chosen);
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
       float h2 = 0.f;
       for (int i = lane; i < f.D / 8; i += 32) {
         float x[8];
-        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(hrow) + i), x);
+        bf16x8_to_f32(reinterpret_cast<const uint4*>(hrow)[i], x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h2 = fmaf(x[k], x[k], h2);
       }

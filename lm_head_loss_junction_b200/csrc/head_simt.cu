@@ -20,10 +20,10 @@ constexpr int kThreads = 256;
 // multiplied.  krow (with !B_K): rows k of B whose .w is 0 count as zeros,
 // whatever they hold.
 template <bool A_K, bool B_K, int TILE>
-__global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict__ A, int64_t lda,
-                                                         const float* __restrict__ B, int64_t ldb,
-                                                         float* __restrict__ C, int64_t ldc, int M, int N, int K,
-                                                         int accumulate, const float4* __restrict__ krow) {
+__global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* A, int64_t lda,
+                                                         const float* B, int64_t ldb,
+                                                         float* C, int64_t ldc, int M, int N, int K,
+                                                         int accumulate, const float4* krow) {
   constexpr int kK = TILE == 16 ? 16 : 32;               // K per slice
   constexpr int kPer = (TILE / 4) * (TILE / 4);          // threads of a group
   constexpr int kGroups = kThreads / kPer;
@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(kThreads) sgemm_kernel(const float* __restrict
       const int ak = A_K ? e % kK : e / TILE, am = A_K ? e / kK : e % TILE;
       const int bk = B_K ? e % kK : e / TILE, bn = B_K ? e / kK : e % TILE;
       const int64_t am_g = m0 + am, bn_g = n0 + bn;
-      ra[i] = am_g < M && k0 + ak < k_end ? __ldg(A + (A_K ? am_g * lda + k0 + ak : (k0 + ak) * lda + am_g)) : 0.f;
+      ra[i] = am_g < M && k0 + ak < k_end ? A[A_K ? am_g * lda + k0 + ak : (k0 + ak) * lda + am_g] : 0.f;
       const bool live = bn_g < N && k0 + bk < k_end && (B_K || krow == nullptr || krow[k0 + bk].w != 0.f);
-      rb[i] = live ? __ldg(B + (B_K ? bn_g * ldb + k0 + bk : (k0 + bk) * ldb + bn_g)) : 0.f;
+      rb[i] = live ? B[B_K ? bn_g * ldb + k0 + bk : (k0 + bk) * ldb + bn_g] : 0.f;
     }
   };
   auto put = [&]() {
@@ -136,8 +136,8 @@ cudaError_t sgemm(const float* A, int64_t lda, const float* B, int64_t ldb, floa
 }
 
 // One warp per (token, split).
-__global__ void __launch_bounds__(256) split_stats_kernel(const float* __restrict__ logits, int64_t ld, int64_t T,
-                                                          int V, int n_splits, HeadPart* __restrict__ part) {
+__global__ void __launch_bounds__(256) split_stats_kernel(const float* logits, int64_t ld, int64_t T,
+                                                          int V, int n_splits, HeadPart* part) {
   after_previous();
   const int lane = threadIdx.x & 31;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* __restric
 }
 
 // Logits -> s (q (A + B (l - lse)) + entries) in place, one block per token.
-__global__ void __launch_bounds__(256) grad_rows_kernel(float* __restrict__ logits, int64_t ld, int V,
+__global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t ld, int V,
                                                         const HeadEntries en, int64_t t0, int64_t T, int n_splits) {
   after_previous();
   const int64_t t = t0 + blockIdx.x;

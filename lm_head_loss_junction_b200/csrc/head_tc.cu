@@ -164,7 +164,7 @@ struct EntryWalk {
   __device__ __forceinline__ int2 load() {
     if (n <= 0) return make_int2(INT32_MAX, 0);
     --n;
-    return __ldg(p++);
+    return *p++;
   }
   __device__ __forceinline__ void start(const TileArgs& a, bool valid, int t, int split) {
     n = 0;
@@ -355,8 +355,8 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       __syncwarp();
     }
   } else {
-    const float alpha = EPI == kDw ? __uint_as_float(__ldg(a.smax)) / kRowLift : __ldg(a.inv);
-    const float rs = EPI == kDh && valid ? __ldg(&a.row[row].w) : 1.f;
+    const float alpha = EPI == kDw ? __uint_as_float(*a.smax) / kRowLift : *a.inv;
+    const float rs = EPI == kDh && valid ? a.row[row].w : 1.f;
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
 #pragma unroll 1
@@ -551,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
       RowAhead ahead;
       if constexpr (EPI == kStats || EPI == kGrad) {
         const int c0 = u.nt * kBN + half * 128;
-        if constexpr (EPI == kGrad) ahead.ri = row < a.rows ? __ldg(a.row + row) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (EPI == kGrad) ahead.ri = row < a.rows ? a.row[row] : make_float4(0.f, 0.f, 0.f, 0.f);
         // (a row of scale 0 has entries, of coefficient 0: its G' is 0 whatever the row holds)
         ahead.en.start(a, row < a.rows && c0 < a.cols, static_cast<int>(row), (a.v0 + c0) / kHeadSplit);
       }
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(256) head_reduce_kernel(const ReduceArgs a) {
     if (own == 0 && a.acc_in) v = a.acc[i];
 #pragma unroll 4
     for (int p = own; p < a.parts; p += kReduceLanes) {
-      const float4 x = __ldg(a.part + p * a.n + i);
+      const float4 x = a.part[p * a.n + i];
       v.x += x.x;
       v.y += x.y;
       v.z += x.z;

@@ -427,6 +427,37 @@ def test_other_stream_and_two_calls_at_once():
         assert all(torch.equal(p, q) for p, q in zip(r, o))
 
 
+@pytest.mark.parametrize("dtype,T", [(BF, 20), (BF, 140), (BF, 600), (F32, 90)])
+def test_inputs_written_just_before_the_call(dtype, T):
+    """The kernels of a call are set up while the one before runs: nothing they read may be from before it."""
+    sets = [_distill_inputs(T, 64, 700, 5, seed=30 + i, dtype=dtype)[1] for i in range(4)]
+    x = [t.clone() for t in sets[0]]
+    y, tid, z, h, W = x
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+
+    def work():
+        losses, stats = topk_distill_fwd(y, tid, z, h, W, workspace=ws)
+        dh, dW = topk_distill_bwd(y, tid, z, h, W, stats, workspace=ws)
+        return [losses, stats, dh, dW, *token_logprobs(y, h, W, top_k=6, workspace=ws)]
+
+    ref = []
+    for s in sets:
+        for d, v in zip(x, s):
+            d.copy_(v)
+        torch.cuda.synchronize()
+        ref.append([t.clone() for t in work()])
+        torch.cuda.synchronize()
+    for turn in range(25):
+        got = []
+        for s in sets:
+            for d, v in zip(x, s):
+                d.copy_(v)
+            got.append(work())
+        torch.cuda.synchronize()
+        for r, g in zip(ref, got):
+            assert all(torch.equal(a, b) for a, b in zip(r, g)), turn
+
+
 def test_captured_and_replayed_with_new_inputs():
     _, x = _distill_inputs(130, 64, 700, 5, seed=3)
     _, x2 = _distill_inputs(130, 64, 700, 5, seed=4)
