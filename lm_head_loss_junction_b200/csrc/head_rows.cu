@@ -258,7 +258,8 @@ __device__ __forceinline__ float fine_base2(double l, float m) {
 // lse is not.  ids: the given tokens; fine: their logits in 64 bits, or NULL.
 __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int lane, float m, float logz, float mean,
                                              const int* ids, const double* fine) {
-  if (lane == 0) f.stats[t] = kLn2 * (m + logz);
+  // rounded once: the backward pass takes every q of the row from it
+  if (lane == 0) f.stats[t] = static_cast<float>(0.6931471805599453 * (static_cast<double>(m) + static_cast<double>(logz)));
   bool bad = false;
   if (f.y == nullptr) {
     if (lane == 0) f.stats[f.ldT + t] = kLn2 * (logz - mean);

@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t l
   float* row = logits + static_cast<int64_t>(blockIdx.x) * ld;
   const float4 ri = en.row[t];
   for (int v = threadIdx.x; v < V; v += 256) {
-    const float d = to_base2(row[v], kLog2e, ri.x * kLog2e);
+    // the difference first: rounding lse log2(e) would cost every q of the row 1e-6 of itself
+    const float d = (row[v] - ri.x) * kLog2e;
     row[v] = ri.w == 0.f ? 0.f : ri.w * (ex2(d) * fmaf(ri.z * kLn2, d, ri.y));
   }
   __syncthreads();
