@@ -12,6 +12,10 @@
  *   mls_multiexit_loss_fwd / _bwd             -- per-exit logits, next-token CE,
  *                                                distillation from the largest
  *                                                exit, and their gradients
+ *   mls_token_logprobs, mls_topk_distill_fwd     -- for one exit alone: log
+ *   and their _bwd                                probabilities of given tokens,
+ *                                                distillation from a teacher's
+ *                                                top logits
  *
  * Conventions shared by every entry point
  *   - All tensors are row-major with tokens outermost, on the current CUDA

@@ -345,10 +345,8 @@ def _head_common(h, W):
     return T, D, V, _dtype_code(h), h.device
 
 
-def _head_stream(stream, dev):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return _stream_ptr(stream)
+def _head_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _head_ids(ids, T, dev):
@@ -377,13 +375,27 @@ def _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW):
     elif want_dW:
         if accumulate_dW:
             raise ValueError("accumulate_dW needs dW")
-        dW = torch.empty(W.shape, dtype=dW_dtype, device=W.device)
+        dW = torch.empty(*W.shape, dtype=dW_dtype, device=W.device)
     return dh, dW, _dtype_code(dW) if dW is not None else MLS_F32
 
 
-def _elsewhere(h):
-    """Whether h lives on another device than the current one (the library launches on the current one)."""
-    return h.is_cuda and h.device.index != torch.cuda.current_device()
+def _elsewhere(h, stream):
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or h.is_cuda and h.device.index != torch.cuda.current_device()
+
+
+def _moved(fn, h, stream, *args, **kw):
+    """fn(*args, **kw) with the device of h current and, where one is given, on `stream`: launches and allocations
+    both (a workspace from another stream's pool could be handed out again while this one still uses it)."""
+    if stream is None:
+        with torch.cuda.device(h.device):
+            return fn(*args, **kw)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=h.device)
+    if stream.device != h.device:
+        raise ValueError("stream must be of the device of h")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def _code_of(dtype):
@@ -408,10 +420,9 @@ def token_logprobs(ids: Optional[torch.Tensor], h: torch.Tensor, W: torch.Tensor
     ids: int32 [T] or [T, N] (-1: no token there), or None with top_k > 0.  Returns (logp of the shape of ids or
     None, stats [2, T] = log-sum-exp and entropy, top_ids [T, top_k] or None, top_logp [T, top_k] or None).
     """
-    if _elsewhere(h):
-        with torch.cuda.device(h.device):
-            return token_logprobs(ids, h, W, top_k=top_k, logp=logp, stats=stats, top_ids=top_ids, top_logp=top_logp,
-                                  workspace=workspace, status=status, stream=stream)
+    if _elsewhere(h, stream):
+        return _moved(token_logprobs, h, stream, ids, h, W, top_k=top_k, logp=logp, stats=stats, top_ids=top_ids,
+                      top_logp=top_logp, workspace=workspace, status=status)
     T, D, V, dt, dev = _head_common(h, W)
     f32 = torch.float32
     N = 0
@@ -425,26 +436,26 @@ def token_logprobs(ids: Optional[torch.Tensor], h: torch.Tensor, W: torch.Tensor
     if logp is not None:
         _head_fit(logp, "logp", f32, ids.shape, dev)
     elif N:
-        logp = torch.empty(ids.shape, dtype=f32, device=dev)
+        logp = torch.empty(*ids.shape, dtype=f32, device=dev)
     if stats is not None:
         _head_fit(stats, "stats", f32, (2, T), dev)
     else:
-        stats = torch.empty((2, T), dtype=f32, device=dev)
+        stats = torch.empty(2, T, dtype=f32, device=dev)
     if top_ids is not None:
         _head_fit(top_ids, "top_ids", torch.int32, (T, top_k), dev)
     elif top_k:
-        top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        top_ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     if top_logp is not None:
         _head_fit(top_logp, "top_logp", f32, (T, top_k), dev)
     elif top_k:
-        top_logp = torch.empty((T, top_k), dtype=f32, device=dev)
+        top_logp = torch.empty(T, top_k, dtype=f32, device=dev)
     if status is not None:
         _head_fit(status, "status", torch.int32, status.shape, dev)
     workspace, ws_bytes = _head_workspace(workspace, nbytes, dev)
     check("mls_token_logprobs",
           lib().mls_token_logprobs(T, D, V, N, _ptr(ids), h.data_ptr(), W.data_ptr(), dt, _ptr(logp),
                                    stats.data_ptr(), top_k, _ptr(top_ids), _ptr(top_logp), workspace.data_ptr(),
-                                   ws_bytes, _ptr(status), _head_stream(stream, dev)))
+                                   ws_bytes, _ptr(status), _head_stream(dev)))
     return logp, stats, top_ids, top_logp
 
 
@@ -464,11 +475,10 @@ def token_logprobs_bwd(ids: torch.Tensor, h: torch.Tensor, W: torch.Tensor, stat
     """Gradients of token_logprobs' log probabilities (g_logp, the shape of ids) and entropies (g_entropy [T])
     with respect to h and W (see mls_token_logprobs_bwd).  Returns (dh or None, dW or None); dW is fp32, or
     bf16 with dW_dtype=torch.bfloat16."""
-    if _elsewhere(h):
-        with torch.cuda.device(h.device):
-            return token_logprobs_bwd(ids, h, W, stats, g_logp, g_entropy, dh=dh, dW=dW, dW_dtype=dW_dtype,
-                                      accumulate_dW=accumulate_dW, want_dh=want_dh, want_dW=want_dW,
-                                      workspace=workspace, status=status, stream=stream)
+    if _elsewhere(h, stream):
+        return _moved(token_logprobs_bwd, h, stream, ids, h, W, stats, g_logp, g_entropy, dh=dh, dW=dW,
+                      dW_dtype=dW_dtype, accumulate_dW=accumulate_dW, want_dh=want_dh, want_dW=want_dW,
+                      workspace=workspace, status=status)
     T, D, V, dt, dev = _head_common(h, W)
     N = _head_ids(ids, T, dev)
     _head_fit(stats, "stats", torch.float32, (2, T), dev)
@@ -483,7 +493,7 @@ def token_logprobs_bwd(ids: torch.Tensor, h: torch.Tensor, W: torch.Tensor, stat
           lib().mls_token_logprobs_bwd(T, D, V, N, ids.data_ptr(), h.data_ptr(), W.data_ptr(), dt,
                                        stats.data_ptr(), g_logp.data_ptr(), _ptr(g_entropy), _ptr(dh), _ptr(dW),
                                        dW_code, int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes,
-                                       _ptr(status), _head_stream(stream, dev)))
+                                       _ptr(status), _head_stream(dev)))
     return dh, dW
 
 
@@ -519,10 +529,9 @@ def topk_distill_fwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
 
     Returns (losses [3] = mean cross-entropy, mean distillation term, their mix; stats [3, T] = log-sum-exp and
     the two terms of every token)."""
-    if _elsewhere(h):
-        with torch.cuda.device(h.device):
-            return topk_distill_fwd(y, teacher_ids, teacher_logits, h, W, alpha_d, token_weights=token_weights,
-                                    losses=losses, stats=stats, workspace=workspace, status=status, stream=stream)
+    if _elsewhere(h, stream):
+        return _moved(topk_distill_fwd, h, stream, y, teacher_ids, teacher_logits, h, W, alpha_d,
+                      token_weights=token_weights, losses=losses, stats=stats, workspace=workspace, status=status)
     T, D, V, K, dt, dev = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status)
     nbytes = topk_distill_workspace(T, D, V, K, h.dtype)[0]
     if losses is not None:
@@ -532,13 +541,13 @@ def topk_distill_fwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
     if stats is not None:
         _head_fit(stats, "stats", torch.float32, (3, T), dev)
     else:
-        stats = torch.empty((3, T), dtype=torch.float32, device=dev)
+        stats = torch.empty(3, T, dtype=torch.float32, device=dev)
     workspace, ws_bytes = _head_workspace(workspace, nbytes, dev)
     check("mls_topk_distill_fwd",
           lib().mls_topk_distill_fwd(T, D, V, K, y.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
                                      _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
                                      losses.data_ptr(), stats.data_ptr(), workspace.data_ptr(), ws_bytes,
-                                     _ptr(status), _head_stream(stream, dev)))
+                                     _ptr(status), _head_stream(dev)))
     return losses, stats
 
 
@@ -549,12 +558,10 @@ def topk_distill_bwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
                      want_dW: bool = True, workspace=None, status=None, stream=None):
     """Gradients of topk_distill_fwd's mixed loss times grad_scale with respect to h and W (see
     mls_topk_distill_bwd).  Returns (dh or None, dW or None)."""
-    if _elsewhere(h):
-        with torch.cuda.device(h.device):
-            return topk_distill_bwd(y, teacher_ids, teacher_logits, h, W, stats, alpha_d, grad_scale,
-                                    token_weights=token_weights, dh=dh, dW=dW, dW_dtype=dW_dtype,
-                                    accumulate_dW=accumulate_dW, want_dh=want_dh, want_dW=want_dW,
-                                    workspace=workspace, status=status, stream=stream)
+    if _elsewhere(h, stream):
+        return _moved(topk_distill_bwd, h, stream, y, teacher_ids, teacher_logits, h, W, stats, alpha_d, grad_scale,
+                      token_weights=token_weights, dh=dh, dW=dW, dW_dtype=dW_dtype, accumulate_dW=accumulate_dW,
+                      want_dh=want_dh, want_dW=want_dW, workspace=workspace, status=status)
     T, D, V, K, dt, dev = _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status)
     _head_fit(stats, "stats", torch.float32, (3, T), dev)
     dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
@@ -564,7 +571,7 @@ def topk_distill_bwd(y: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits:
                                      _ptr(token_weights), h.data_ptr(), W.data_ptr(), float(alpha_d), dt,
                                      stats.data_ptr(), float(grad_scale), _ptr(dh), _ptr(dW), dW_code,
                                      int(bool(accumulate_dW)), workspace.data_ptr(), ws_bytes, _ptr(status),
-                                     _head_stream(stream, dev)))
+                                     _head_stream(dev)))
     return dh, dW
 
 

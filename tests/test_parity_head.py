@@ -427,6 +427,30 @@ def test_other_stream_and_two_calls_at_once():
         assert all(torch.equal(p, q) for p, q in zip(r, o))
 
 
+def test_stream_argument_owns_its_buffers():
+    """On a stream given by argument, as an object or a handle: outputs and workspace come from its own pool, so work
+    on the current stream that reuses freed memory meanwhile does not touch them."""
+    _, x = _distill_inputs(600, 128, 5000, 9, seed=40)
+    losses, stats = topk_distill_fwd(*x)
+    ref = [losses, stats, *topk_distill_bwd(*x, stats), *token_logprobs(x[0], x[3], x[4], top_k=7)]
+    grad = token_logprobs_bwd(x[0], x[3], x[4], ref[5], torch.ones(600, device="cuda"))
+    one = torch.ones(600, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        s.wait_stream(torch.cuda.current_stream())
+        got = []
+        for _ in range(10):
+            l, st = topk_distill_fwd(*x, stream=stream)
+            got = [l, st, *topk_distill_bwd(*x, st, stream=stream), *token_logprobs(x[0], x[3], x[4], top_k=7, stream=stream)]
+            g2 = token_logprobs_bwd(x[0], x[3], x[4], got[5], one, stream=stream)
+            for n in (1 << 20, 1 << 24, 1 << 27):      # what the current stream is handed out next, it overwrites
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+        assert all(torch.equal(a, b) for a, b in zip(grad, g2))
+
+
 @pytest.mark.parametrize("dtype,T", [(BF, 20), (BF, 140), (BF, 600), (F32, 90)])
 def test_inputs_written_just_before_the_call(dtype, T):
     """The kernels of a call are set up while the one before runs: nothing they read may be from before it."""
