@@ -206,6 +206,14 @@ __device__ __forceinline__ void stage_row(uint8_t* stage, int lane, const float 
   for (int k = 0; k < 8; ++k) *staged(stage, lane, k) = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
 }
 
+// Tells the leader that an accumulator buffer was read.  Relaxed: what it orders
+// are TMEM reads, which are complete (tcgen05.wait::ld) and fenced; a release
+// would also wait for the epilogue's global stores to be acknowledged, about a
+// microsecond per tile.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // A_MN / B_MN: the operand is stored with its M / N dimension contiguous
 // (boxes of 64 x 64), otherwise with K contiguous.
 template <Epi EPI>
@@ -223,7 +231,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
   auto release = [&]() {
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+    if (lane == 0) arrive_relaxed(mapa_shared(smem_u32(tempty), 0));
   };
   if constexpr (EPI == kStats || EPI == kLogits) {
     if (c0 >= a.cols) {
