@@ -206,6 +206,24 @@ __device__ __forceinline__ void stage_row(uint8_t* stage, int lane, const float 
   for (int k = 0; k < 8; ++k) *staged(stage, lane, k) = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
 }
 
+// This lane's row of 32 values as 16-bit pairs through the staging rows (of 80
+// bytes here), so that a store instruction writes 8 rows x 64 contiguous bytes:
+// dst is this lane's piece (row lane / 4, 16 bytes lane % 4) of the chunk's
+// first 8 rows, `left` the rows from there on that exist.
+__device__ __forceinline__ void store_pairs(uint8_t* stage, int lane, const uint32_t (&w)[16], uint8_t* dst,
+                                            int64_t row_bytes, int64_t left) {
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStageRow);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mine[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  __syncwarp();
+  const uint8_t* src = stage + (lane >> 2) * kStageRow + (lane & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (8 * i < left)
+      *reinterpret_cast<uint4*>(dst + 8 * i * row_bytes) = *reinterpret_cast<const uint4*>(src + 8 * i * kStageRow);
+  __syncwarp();
+}
+
 // Tells the leader that an accumulator buffer was read.  Relaxed: what it orders
 // are TMEM reads, which are complete (tcgen05.wait::ld) and fenced; a release
 // would also wait for the epilogue's global stores to be acknowledged, about a
@@ -313,7 +331,9 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     const float lse2 = ri.x * kLog2e, A = ri.y, B2 = ri.z * kLn2;
     EntryWalk& en = ahead.en;
     uint8_t* stage = s.stage[warp - 2];
-    const int64_t row0 = row - lane;
+    const int64_t piece_row = row - lane + (lane >> 2);
+    const int64_t left_rows = a.rows - piece_row;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(a.G + piece_row * a.ld + c0 + (lane & 3) * 8);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float r[32];
@@ -347,26 +367,34 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
         }
         __syncwarp();                      // the rows below lie across these
       }
-      uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStageRow);
+      uint32_t w[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mine[k] = make_uint4(pack_g2(r[8 * k], r[8 * k + 1]), pack_g2(r[8 * k + 2], r[8 * k + 3]),
-                             pack_g2(r[8 * k + 4], r[8 * k + 5]), pack_g2(r[8 * k + 6], r[8 * k + 7]));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {        // 8 rows x 64 contiguous bytes per store instruction
-        const int piece = i * 32 + lane;
-        const int rr = piece >> 2, ch = piece & 3;
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * kStageRow + ch * 16);
-        if (row0 + rr < a.rows) *reinterpret_cast<uint4*>(a.G + (row0 + rr) * a.ld + col + ch * 8) = v;
-      }
-      __syncwarp();
+      for (int k = 0; k < 16; ++k) w[k] = pack_g2(r[2 * k], r[2 * k + 1]);
+      store_pairs(stage, lane, w, dst + c * 64, a.ld * 2, left_rows);
     }
   } else {
     const float alpha = EPI == kDw ? __uint_as_float(*a.smax) / kRowLift : *a.inv;
-    const float rs = EPI == kDh && valid ? a.row[row].w : 1.f;
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
+    if (OUT_BF16 && (EPI == kDw || a.acc == nullptr)) {
+      const float f = EPI == kDh ? (valid ? alpha * a.row[row].w : 0.f) : alpha;
+      const int64_t piece_row = row0 + (lane >> 2);
+      uint8_t* dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + piece_row * a.cols + c0 + (lane & 3) * 8);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float r[32];
+        tmem_ld32(acc_col + c * 32, r);
+        if (c == 3) release();
+        if (c0 + c * 32 >= a.cols) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(r[2 * k] * f, r[2 * k + 1] * f);
+        store_pairs(stage, lane, w, dst + c * 64, static_cast<int64_t>(a.cols) * 2, a.rows - piece_row);
+      }
+      return;
+    }
+    // fp32 out, or earlier chunks' sums to add before the rounding: fp32 through the staging rows
+    const float rs = EPI == kDh && valid ? a.row[row].w : 1.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float r[32];
@@ -378,38 +406,21 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       for (int k = 0; k < 32; ++k) r[k] *= alpha;
       stage_row(stage, lane, r);
       __syncwarp();
-      if constexpr (OUT_BF16) {
-        // a store instruction writes 8 rows x 64 contiguous bytes
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2), ch = lane & 3;
-          const float scale = __shfl_sync(0xffffffffu, rs, rr);
-          if (row0 + rr >= a.rows) continue;
-          const int64_t off = (row0 + rr) * a.cols + col + ch * 8;
-          float4 v[2] = {*staged(stage, rr, 2 * ch), *staged(stage, rr, 2 * ch + 1)};
-          if (EPI == kDh && a.acc != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 o = reinterpret_cast<const float4*>(a.acc + off)[j];
-              v[j].x += o.x;
-              v[j].y += o.y;
-              v[j].z += o.z;
-              v[j].w += o.w;
-            }
-          }
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off) =
-              make_uint4(pack_bf16x2(v[0].x * scale, v[0].y * scale), pack_bf16x2(v[0].z * scale, v[0].w * scale),
-                         pack_bf16x2(v[1].x * scale, v[1].y * scale), pack_bf16x2(v[1].z * scale, v[1].w * scale));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = i * 4 + (lane >> 3), ch = lane & 7;
-          if (row0 + rr >= a.rows) continue;
-          float4 v = *staged(stage, rr, ch);
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+        const float scale = __shfl_sync(0xffffffffu, rs, rr);
+        if (row0 + rr >= a.rows) continue;
+        float4 v = *staged(stage, rr, ch);
+        const int64_t off = (row0 + rr) * a.cols + col + ch * 4;
+        if constexpr (OUT_BF16) {
+          const float4 o = *reinterpret_cast<const float4*>(a.acc + off);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off) =
+              make_uint2(pack_bf16x2((v.x + o.x) * scale, (v.y + o.y) * scale),
+                         pack_bf16x2((v.z + o.z) * scale, (v.w + o.w) * scale));
+        } else {
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
-                                                  static_cast<int64_t>(part) * a.rows * a.cols +
-                                                  (row0 + rr) * a.cols + col + ch * 4);
+                                                  static_cast<int64_t>(part) * a.rows * a.cols + off);
           if (a.accumulate) {
             const float4 o = *dst;
             v.x += o.x;
