@@ -12,7 +12,9 @@
 // adds in fp32: shorter runs, smaller error.
 //
 // The logits go to the workspace (T x V fp32, a small part of W's bytes) with
-// the partial statistics of each 128 columns.
+// the partial statistics of each 128 columns.  T = 1, V = 49152, D = 2304: 41 us,
+// T = 24, D = 1024: 22 us (W at 5.9 TB/s after 5 to 7 us of start and tail; the
+// large tiles took 62 and 29 us).
 #include <cuda.h>
 
 #include "head.h"
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
     tmem_relinquish();
   }
   // The thread that made the barriers is the one that loads: its first loads are on their way before the other warps
-  // are set up.  (block g of the first tile is kb = g: a tile shorter than the ring starts with its own blocks only)
+  // are set up (the first tile's K blocks, as many as the ring holds).
   after_previous();
   const int early = static_cast<int>(blockIdx.x) < a.n_tiles ? (a.kblocks < kStages ? a.kblocks : kStages) : 0;
   if (threadIdx.x == 0) {

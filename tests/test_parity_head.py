@@ -507,6 +507,46 @@ def test_captured_and_replayed_with_new_inputs():
         assert all(torch.equal(p, q) for p, q in zip(got, step()))
 
 
+FIRST_CAPTURED = """
+import torch
+from lm_head_loss_junction_b200 import token_logprobs, token_logprobs_bwd, topk_distill_bwd, topk_distill_fwd
+g = torch.Generator(device="cuda").manual_seed(0)
+def data(T, D, V, K, dt):
+    h = torch.randn(T, D, generator=g, device="cuda").to(dt)
+    W = torch.randn(V, D, generator=g, device="cuda").to(dt)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    return h, W, ids, torch.randn(T, K, generator=g, device="cuda")
+sets = [data(*x) for x in [(20, 64, 300, 3, torch.bfloat16), (600, 128, 700, 5, torch.bfloat16), (30, 9, 70, 2, torch.float32)]]
+def work():
+    out = []
+    for h, W, ids, z in sets:
+        y = ids[:, 0].contiguous()
+        lp, st, a, b = token_logprobs(ids, h, W, top_k=4)
+        l, s = topk_distill_fwd(y, ids, z, h, W)
+        out += [lp, st, a, b, *token_logprobs_bwd(ids, h, W, st, z), l, s, *topk_distill_bwd(y, ids, z, h, W, s)]
+    return out
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = work()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in out]
+assert all(torch.equal(p, q) for p, q in zip(got, work()))
+print("captured first")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """No call needs a warm-up before it is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
 def test_outputs_stay_inside_their_buffers():
     from tests.test_guards import Guarded
     for dtype, T, D, V, K in ((BF, 131, 64, 333, 7), (F32, 31, 37, 201, 5)):
