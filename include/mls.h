@@ -523,10 +523,11 @@ mls_status mls_token_logprobs(int64_t T, int64_t D, int64_t V, int N, const int3
  *              are not read as gradients)
  *   g_entropy  device f32 [T], finite, or NULL (0)
  * The alternatives are given tokens too: pass their ids and gradients.
- * MLS_BF16: dL/dl is formed in fp16 (11-bit significand, each row over a power
- * of two near its largest coefficient) for one chunk of the vocabulary at a
- * time, and multiplied on the tensor cores with fp16 copies of W and h, fp32
- * sums.
+ * MLS_BF16: dL/dl is formed in fp16 (11-bit significand) for one chunk of the
+ * vocabulary at a time, each row over a power of two that brings the sum of its
+ * coefficients' magnitudes to 2^14: an entry below 2^-28 of that sum has fewer
+ * bits, one below 2^-39 of it is 0.  It is multiplied on the tensor cores with
+ * fp16 copies of W and h, fp32 sums.
  */
 mls_status mls_token_logprobs_bwd_workspace(int64_t T, int64_t D, int64_t V, int N, mls_dtype dt,
                                             size_t* bytes, size_t* min_bytes);

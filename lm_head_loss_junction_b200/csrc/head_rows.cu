@@ -33,10 +33,16 @@ struct EntrySmem {
   int count[kEntryTokens];
 };
 
-__device__ __forceinline__ float pow2_of(float m) {
-  if (!(m > 0.f) || !(m <= 3.4e38f)) return m == 0.f ? 0.f : 1.f;
-  int e = ilogbf(m);
-  e = e < -126 ? -126 : (e > 126 ? 126 : e);
+// The power of two s_t that brings a row of G into [2^14, 2^15) at its bound:
+// G' = G / s_t fills fp16's range from the top, so a probability keeps 11 bits
+// down to 2^-28 of the bound and counts down to 2^-39.  (With the bound brought
+// to 1, what fell below 2^-24 of it was lost: a row's small probabilities all
+// have one sign, and of a row with q_y = 0.9997 over 49152 columns half the
+// gradient went.)  1 where the bound is no number, which the row then shows.
+__device__ __forceinline__ float row_scale(float bound) {
+  if (!(bound > 0.f)) return bound == 0.f ? 0.f : 1.f;
+  int e = ilogbf(fminf(bound, 3.4e38f)) - 14;
+  e = e < -126 ? -126 : e;
   return ldexpf(1.f, e);
 }
 
@@ -92,19 +98,20 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
     }
     float A = 0.f, B = 0.f, scale = 0.f;
     if (backward) {
-      float most = 0.f;
+      float bound = 0.f;                   // on |G| of the row
       if (in.y == nullptr) {
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
           if (there[k]) c[k] = in.g_logp[t * N + k * 32 + lane];
           sum += c[k];
-          most = fmaxf(most, fabsf(c[k]));
+          bound += fabsf(c[k]);
         }
         sum = warp_sum(sum);
         B = in.g_entropy != nullptr ? -in.g_entropy[t] : 0.f;
         A = -sum + (in.g_entropy != nullptr ? B * in.stats[in.T + t] : 0.f);
-        most = fmaxf(warp_max(most), fmaxf(fabsf(sum), fabsf(B)));
+        // q (H + log q) is largest where one token holds about half and the rest is flat: under 7 for V < 2^31
+        bound = warp_sum(bound) + fabsf(sum) + 7.f * fabsf(B);
       } else {
         float z[kPerLane], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -126,12 +133,12 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
         for (int k = 0; k < kPerLane; ++k) {
           const int j = k * 32 + lane;
           if (there[k]) c[k] = j == N ? -wg * (1.f - in.alpha) : (some ? -wg * in.alpha * (z[k] / sum) : 0.f);
-          most = fmaxf(most, fabsf(c[k]));
+          bound += fabsf(c[k]);
         }
         A = wg * ((1.f - in.alpha) + (some ? in.alpha : 0.f));
-        most = fmaxf(warp_max(most), fabsf(A));
+        bound = warp_sum(bound) + fabsf(A);
       }
-      scale = pow2_of(most);
+      scale = row_scale(bound);
       if (lane == 0) {
         const float r = scale != 0.f ? 1.f / scale : 0.f;
         out.row[t] = make_float4(in.stats[t], A * r, B * r, scale);

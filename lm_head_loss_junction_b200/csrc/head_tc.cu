@@ -20,9 +20,10 @@
 //
 // G' is fp16 (11-bit significand), not bf16 (8): the few large entries of a
 // peaked row dominate the gradient's error.  A row is stored divided by a
-// power of two s_t near the row's largest coefficient, so that rows of very
-// different weight keep the same relative precision; dh multiplies by s_t in
-// the epilogue and dw reads h rows that were multiplied by s_t when they were
+// power of two s_t that brings its bound to 2^14, so that rows of very
+// different weight keep the same relative precision and the small
+// probabilities of a peaked row keep theirs; dh multiplies by s_t in the
+// epilogue and dw reads h rows that were multiplied by s_t when they were
 // copied to fp16 (powers of two change no significand).
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -380,7 +381,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
     if (OUT_BF16 && (EPI == kDw || a.acc == nullptr)) {
-      const float f = EPI == kDh ? (valid ? alpha * a.row[row].w : 0.f) : alpha;
+      const float f = EPI == kDh && valid ? a.row[row].w : 1.f;     // apart from alpha: their product can underflow
       const int64_t piece_row = row0 + (lane >> 2);
       uint8_t* dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + piece_row * a.cols + c0 + (lane & 3) * 8);
 #pragma unroll 1
@@ -391,7 +392,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
         if (c0 + c * 32 >= a.cols) continue;
         uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(r[2 * k] * f, r[2 * k + 1] * f);
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(r[2 * k] * alpha * f, r[2 * k + 1] * alpha * f);
         store_pairs(stage, lane, w, dst + c * 64, static_cast<int64_t>(a.cols) * 2, a.rows - piece_row);
       }
       return;
