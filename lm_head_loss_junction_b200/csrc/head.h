@@ -105,6 +105,19 @@ struct HeadCopyH {
 cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bool backward, int32_t* status,
                              const HeadCopyW* w, cudaStream_t st);
 
+// G' of a chunk of the vocabulary, whose entries of much weight are formed again
+// from products in 64 bits (bf16; head_exact.cuh).
+struct HeadExact {
+  int64_t T, D;
+  const void* h;
+  const void* W;                   // the whole of it
+  HeadEntries en;
+  __half* G;                       // [T][ld], column 0 is id v0
+  int64_t ld, v0, n;
+};
+// w (may be NULL): a copy of W that further blocks of the launch give its scale.
+cudaError_t run_head_exact(const HeadExact& x, const HeadCopyW* w, cudaStream_t st);
+
 // ------------------------------------------------------------------ per-token results
 struct HeadFinish {
   int64_t T, V;                    // tokens of this launch

@@ -6,6 +6,7 @@
 #include "head.h"
 #include "head_copy.cuh"
 #include "head_dev.cuh"
+#include "head_exact.cuh"
 #include "head_host.h"
 
 namespace mls {
@@ -216,6 +217,32 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
   }
 }
 
+// ------------------------------------------------------------------ entries of the gradient that hold much of a row
+// G' of a chunk's entries again where they hold more than about 2^-5 of their
+// row, from products in 64 bits (head_exact.cuh).  Blocks past the tokens' give
+// the chunk's fp16 copy of W its scale.
+__global__ void __launch_bounds__(256) head_exact_kernel(const HeadExact x, unsigned token_blocks, const HeadCopyW w_copy) {
+  after_previous();
+  if (blockIdx.x >= token_blocks) {
+    rescale_w(w_copy, static_cast<int64_t>(blockIdx.x - token_blocks) * 256 + threadIdx.x,
+              static_cast<int64_t>(gridDim.x - token_blocks) * 256);
+    return;
+  }
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= x.T) return;
+  const float4 ri = x.en.row[t];
+  if (ri.w == 0.f) return;
+  __half* row = x.G + t * x.ld;            // of ids from v0
+  const int begin = x.en.first[x.v0 / kHeadSplit * x.T + t];
+  const int end = x.en.first[(x.v0 + x.n + kHeadSplit - 1) / kHeadSplit * x.T + t];
+  exact_entries<true>(
+      x.en.e + t * x.en.Ntot, begin, end, ri, static_cast<const char*>(x.h) + t * x.D * 2, x.W, x.D, threadIdx.x & 31,
+      [&](int id, float sum) { return __half2float(row[id - x.v0]) - sum; },
+      [&](int id, float v, bool heavy) {
+        if (heavy) row[id - x.v0] = __float2half_rn(fabsf(v) > 65504.f ? copysignf(65504.f, v) : v);
+      });
+}
+
 // ------------------------------------------------------------------ merge of partial statistics
 // (m, z, u) of two column sets -> of their union.
 __device__ __forceinline__ void merge_part(float& m, float& z, float& u, float m2, float z2, float u2) {
@@ -260,56 +287,112 @@ __device__ __forceinline__ float fine_base2(double l, float m) {
   return static_cast<float>(fma(l, 1.4426950408889634, -static_cast<double>(m)));
 }
 
+// The token's own numbers, entry k * 32 + lane of a warp's: the given tokens, or the teacher's and then the target.
+struct Given {
+  int id[kPerLane];
+  bool there[kPerLane];
+  float d[kPerLane];               // logits to base 2, over the row's reference
+  bool bad, out;                   // an id, the target outside the vocabulary (then no logit was picked)
+};
+
+// ids: the token's; fine: their logits in 64 bits, or NULL.
+__device__ __forceinline__ Given load_given(const HeadFinish& f, int64_t t, int lane, float m, const int* ids,
+                                            const double* fine) {
+  Given g;
+  const int tot = f.N + (f.y != nullptr ? 1 : 0);
+  const int y = f.y != nullptr ? f.y[t] : 0;
+  g.bad = false;
+  g.out = f.y != nullptr && (y < 0 || y >= f.V);
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    const int j = k * 32 + lane;
+    g.id[k] = j < f.N ? ids[j] : j < tot ? y : -1;
+    g.there[k] = g.id[k] >= 0 && g.id[k] < f.V;
+    g.bad |= j < f.N && !g.there[k] && g.id[k] != -1;
+    g.d[k] = 0.f;
+    if (g.there[k] && !g.out)
+      g.d[k] = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, tot, j, g.id[k]), f.log2e, m);
+  }
+  return g;
+}
+
+// The entries that hold more than 2^-4 of their row (at most 16 of them): their logits from products in 64 bits, and
+// their terms of z and u with them.  The gradient of such an entry is a small difference, q less its coefficient, and
+// is formed from these products too (head_exact.cuh), so it agrees with the log-sum-exp to fp32 rounding, whichever
+// kernel made that of whatever batch.
+template <bool BF16>
+__device__ __forceinline__ void refine_given(const HeadFinish& f, int64_t t, int lane, float m, float& z, float& u,
+                                             Given& g) {
+  const float least = log2f(z) - 4.f;
+  const char* h = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    unsigned todo = __ballot_sync(kFull, g.there[k] && !g.out && g.d[k] > least);
+    while (todo != 0) {
+      const int src = __ffs(todo) - 1;
+      const int id[1] = {__shfl_sync(kFull, g.id[k], src)};
+      const float was = __shfl_sync(kFull, g.d[k], src);
+      bool before = false;                                 // named already: its terms are replaced
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) before |= i < k && g.id[i] == id[0];
+      todo &= ~__ballot_sync(kFull, g.id[k] == id[0]);
+      if (__any_sync(kFull, before)) continue;
+      double l[1];
+      dots64<BF16, 1>(h, f.W, f.D, id, lane, l);
+      const float is = fine_base2(l[0], m);
+      const float e0 = ex2(was), e1 = ex2(is);
+      z += e1 - e0;
+      u += is * e1 - was * e0;
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i)
+        if (g.id[i] == id[0]) g.d[i] = is;
+    }
+  }
+}
+
 // The token's outputs that need only the statistics, by one warp.  A log
 // probability is ln 2 ((l log2(e) - m) - log2 z): both are small where it is,
-// lse is not.  ids: the given tokens; fine: their logits in 64 bits, or NULL.
+// lse is not.
 __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int lane, float m, float logz, float mean,
-                                             const int* ids, const double* fine) {
+                                             const Given& g) {
   // rounded once: the backward pass takes every q of the row from it
   if (lane == 0) f.stats[t] = static_cast<float>(0.6931471805599453 * (static_cast<double>(m) + static_cast<double>(logz)));
-  bool bad = false;
+  bool bad = g.bad;
   if (f.y == nullptr) {
     if (lane == 0) f.stats[f.ldT + t] = kLn2 * (logz - mean);
-    for (int j = lane; j < f.N; j += 32) {
-      const int id = ids[j];
-      const bool there = id >= 0 && id < f.V;
-      float d = 0.f;
-      if (there) d = fine != nullptr ? fine_base2(fine[j], m) : to_base2(entry_logit(f, t, f.N, j, id), f.log2e, m);
-      f.logp[t * f.N + j] = there ? kLn2 * (d - logz) : 0.f;
-      bad |= !there && id != -1;
-    }
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k)
+      if (k * 32 + lane < f.N) f.logp[t * f.N + k * 32 + lane] = g.there[k] ? kLn2 * (g.d[k] - logz) : 0.f;
   } else {
-    const int tot = f.N + 1;
     const float w = f.weights != nullptr ? f.weights[t] : 1.f;
-    const int y = f.y[t];
-    const bool out = y < 0 || y >= f.V;      // its logits were not picked
-    bad = out && w != 0.f;
-    float top = -INFINITY;
-    for (int j = lane; j < f.N; j += 32) {
-      const int id = f.ids[t * f.N + j];
-      const bool there = id >= 0 && id < f.V;
-      if (there) top = fmaxf(top, f.teacher[t * f.N + j]);
-      bad |= !there && id != -1;
+    bad |= g.out && w != 0.f;
+    float z[kPerLane], top = -INFINITY, dy = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int j = k * 32 + lane;
+      z[k] = j < f.N && g.there[k] ? f.teacher[t * f.N + j] : -INFINITY;
+      top = fmaxf(top, z[k]);
+      if (j == f.N) dy = g.d[k];
     }
     top = warp_max(top);
+    dy = __shfl_sync(kFull, dy, f.N & 31);
     const bool some = top > -INFINITY;
     float sum = 0.f, kd = 0.f;
-    if (some && !out)
-      for (int j = lane; j < f.N; j += 32) {
-        const int id = f.ids[t * f.N + j];
-        if (id < 0 || id >= f.V) continue;
-        const float p = expf(f.teacher[t * f.N + j] - top);
-        sum += p;
-        if (p != 0.f) kd = fmaf(p, logz - to_base2(entry_logit(f, t, tot, j, id), f.log2e, m), kd);
-      }
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      if (!some || g.out || k * 32 + lane >= f.N || !g.there[k]) continue;
+      const float p = expf(z[k] - top);
+      sum += p;
+      if (p != 0.f) kd = fmaf(p, logz - g.d[k], kd);
+    }
     sum = warp_sum(sum);
     kd = warp_sum(kd);
-    kd = some && !out ? kLn2 * (kd / sum) : 0.f;
+    kd = some && !g.out ? kLn2 * (kd / sum) : 0.f;
     if (lane == 0) {
-      const float ce = out ? 0.f : kLn2 * (logz - to_base2(entry_logit(f, t, tot, f.N, y), f.log2e, m));
+      const float ce = g.out ? 0.f : kLn2 * (logz - dy);
       f.stats[f.ldT + t] = ce;
       f.stats[2 * f.ldT + t] = kd;
-      const bool counts = !out && w != 0.f;  // 0 times a term that is not a number is not 0
+      const bool counts = !g.out && w != 0.f;  // 0 times a term that is not a number is not 0
       const float wce = counts ? w * ce : 0.f, wkd = counts ? w * kd : 0.f;
       f.terms[t] = wce;
       f.terms[f.ldT + t] = wkd;
@@ -317,6 +400,14 @@ __device__ __forceinline__ void finish_token(const HeadFinish& f, int64_t t, int
     }
   }
   if (__any_sync(kFull, bad) && lane == 0) set_flag(f.status, MLS_DEVFLAG_BAD_ID);
+}
+
+// A token from its row's merged statistics.
+template <bool BF16>
+__device__ __forceinline__ void finish_merged(const HeadFinish& f, int64_t t, int lane, float m, float z, float u) {
+  Given g = load_given(f, t, lane, m, f.ids + t * f.N, nullptr);
+  refine_given<BF16>(f, t, lane, m, z, u, g);
+  finish_token(f, t, lane, m, log2f(z), u / z, g);
 }
 
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
@@ -330,7 +421,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish f) {
     merge_part(m, z, u, p.x, p.y, p.z);
   }
   warp_merge(m, z, u);
-  finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+  finish_merged<true>(f, t, lane, m, z, u);
 }
 
 // The same for the few tokens of one block, and the means of their loss terms:
@@ -346,7 +437,7 @@ __global__ void __launch_bounds__(1024) head_finish_loss_kernel(const HeadFinish
       merge_part(m, z, u, p.x, p.y, p.z);
     }
     warp_merge(m, z, u);
-    finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+    finish_merged<true>(f, t, lane, m, z, u);
   }
   __syncthreads();
   if (warp < 3) {
@@ -388,7 +479,7 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
   if (warp != 0) return;
   z = warp_sum(lane < 8 ? sz[lane] : 0.f);
   u = warp_sum(lane < 8 ? su[lane] : 0.f);
-  finish_token(f, t, lane, m, log2f(z), u / z, f.ids + t * f.N, nullptr);
+  finish_merged<false>(f, t, lane, m, z, u);
 }
 
 // ------------------------------------------------------------------ top alternatives
@@ -489,50 +580,7 @@ __device__ uint64_t select_kth(const Keys& keys, int n, int k, int* hist, int* c
   return prefix;
 }
 
-// Products h . W[id[g]] in 64 bits of G rows of W at once (their loads in
-// flight together), by one warp; lane 0's results count.
-template <bool BF16, int G>
-__device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, const int* id, int lane,
-                                       double (&acc)[G]) {
-#pragma unroll
-  for (int g = 0; g < G; ++g) acc[g] = 0.0;
-  if constexpr (BF16) {
-    // a product of two bf16 values is exact in fp32
-    const uint4* a = static_cast<const uint4*>(h);
-    const uint4* b[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) b[g] = static_cast<const uint4*>(W) + id[g] * (D / 8);
-    const int n = static_cast<int>(D / 8);
-#pragma unroll(G == 1 ? 4 : 1)
-    for (int i = lane; i < n; i += 32) {
-      uint4 w[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) w[g] = b[g][i];
-      float x[8];
-      bf16x8_to_f32(a[i], x);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float y[8];
-        bf16x8_to_f32(w[g], y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[g] += static_cast<double>(x[k] * y[k]);
-      }
-    }
-  } else {
-    const float* a = static_cast<const float*>(h);
-    for (int64_t i = lane; i < D; i += 32) {
-      const double x = a[i];
-#pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = fma(x, static_cast<double>(static_cast<const float*>(W)[id[g] * D + i]), acc[g]);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(kFull, acc[g], o);
-}
-
-// The same with fp32 sums of 8 products, and the squared norms of the rows.
+// Products as dots64's with fp32 sums of 8 of them, and the squared norms of the rows.
 template <int G>
 __device__ __forceinline__ void dots_fast(const void* h, const void* W, int64_t D, const int* id, int lane,
                                           double (&acc)[G], float (&w2)[G]) {
@@ -836,7 +884,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   du = warp_sum(du);
   z += dz;
   const float logz = log2f(z);
-  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, s.given, s.fine);
+  if (warp == 0) finish_token(f, t, lane, m, logz, (u + du) / z, load_given(f, t, lane, m, s.given, s.fine));
   if (r < have && rank < f.K) {
     f.top_ids[t * f.K + rank] = s.id[f.N + r];
     f.top_logp[t * f.K + rank] = kLn2 * (fine_base2(fine[r], m) - logz);
@@ -882,6 +930,12 @@ cudaError_t run_head_entries(const HeadEntriesIn& in, const HeadEntries& out, bo
   const unsigned more = w != nullptr ? head_copy_blocks(w->n_vec) : 0;
   return head_launch(head_entries_kernel, dim3(grid + more), 256, 0, st, in, out, backward,
                      static_cast<int>(head_splits(in.V)), grid, w != nullptr ? *w : HeadCopyW{}, status);
+}
+
+cudaError_t run_head_exact(const HeadExact& x, const HeadCopyW* w, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((x.T + 7) / 8);
+  const unsigned more = w != nullptr ? head_copy_blocks(w->n_vec) : 0;
+  return head_launch(head_exact_kernel, dim3(grid + more), 256, 0, st, x, grid, w != nullptr ? *w : HeadCopyW{});
 }
 
 cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {

@@ -4,6 +4,7 @@
 // latency there (a handful of 64 x 64 tiles).
 #include "head.h"
 #include "head_dev.cuh"
+#include "head_exact.cuh"
 #include "head_host.h"
 
 namespace mls {
@@ -165,9 +166,11 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* logits, i
   if (lane == 0) part[i] = make_float4(m, z, u, top);
 }
 
-// Logits -> s (q (A + B (l - lse)) + entries) in place, one block per token.
-__global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t ld, int V,
-                                                        const HeadEntries en, int64_t t0, int64_t T, int n_splits) {
+// Logits -> s (q (A + B (l - lse)) + entries) in place, one block per token; h: the
+// rows of the block of tokens.
+__global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t ld, int V, const HeadEntries en,
+                                                        const float* h, const float* W, int64_t D, int64_t t0, int64_t T,
+                                                        int n_splits) {
   after_previous();
   const int64_t t = t0 + blockIdx.x;
   float* row = logits + static_cast<int64_t>(blockIdx.x) * ld;
@@ -178,12 +181,12 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t l
     row[v] = ri.w == 0.f ? 0.f : ri.w * (ex2(d) * fmaf(ri.z * kLn2, d, ri.y));
   }
   __syncthreads();
-  if (threadIdx.x == 0 && ri.w != 0.f) {
-    const int n = en.first[static_cast<int64_t>(n_splits) * T + t];
-    for (int i = 0; i < n; ++i) {
-      const int2 e = en.e[t * en.Ntot + i];
-      row[e.x] += ri.w * __int_as_float(e.y);
-    }
+  if (threadIdx.x < 32 && ri.w != 0.f) {
+    const float over = 1.f / ri.w;
+    exact_entries<false>(
+        en.e + t * en.Ntot, 0, en.first[static_cast<int64_t>(n_splits) * T + t], ri,
+        h + static_cast<int64_t>(blockIdx.x) * D, W, D, threadIdx.x, [&](int id, float) { return row[id] * over; },
+        [&](int id, float v, bool) { row[id] = ri.w * v; });
   }
 }
 
@@ -209,7 +212,7 @@ cudaError_t head_simt_backward(const HeadProblem& p, const HeadEntries& en, floa
     cudaError_t err = head_simt_logits(p, t0, n, logits, ld, nullptr, st);
     if (err != cudaSuccess) return err;
     err = head_launch(grad_rows_kernel, dim3(static_cast<unsigned>(n)), 256, 0, st, logits, ld, static_cast<int>(p.V),
-                      en, t0, p.T, static_cast<int>(head_splits(p.V)));
+                      en, static_cast<const float*>(p.h) + t0 * p.D, W, p.D, t0, p.T, static_cast<int>(head_splits(p.V)));
     if (err != cudaSuccess) return err;
     if (dh != nullptr) {
       err = sgemm<true, false>(logits, ld, W, p.D, dh + t0 * p.D, p.D, n, p.D, p.V, 0, nullptr, p.T, st);

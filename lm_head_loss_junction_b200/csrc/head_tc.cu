@@ -55,16 +55,10 @@ constexpr float kMasked = -1.0e38f;      // logit of a column past V: finite to 
 
 enum Epi { kStats, kLogits, kGrad, kDh, kDw };
 
-// W's copy in a kernel of its own (later chunks of few tokens), and its scale.
+// W's copy in a kernel of its own (later chunks of few tokens).
 __global__ void __launch_bounds__(256) head_copy_kernel(const HeadCopyW w) {
   after_previous();
   copy_w(w, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, static_cast<int64_t>(gridDim.x) * blockDim.x);
-}
-
-__global__ void __launch_bounds__(256) head_rescale_kernel(const HeadCopyW w) {
-  after_previous();
-  rescale_w(w, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
-            static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 struct TileMaps {
@@ -909,10 +903,9 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntriesIn& in, cons
       a.copy_h = HeadCopyH{p.h, h16, p.T * p.D / 8, static_cast<int>(p.D / 8), en.row, en.smax};
     err = run_tiles<kGrad, false>(maps, a, p.D, 1, st);
     if (err != cudaSuccess) return err;
-    if (dh != nullptr && beside) {
-      err = head_launch(head_rescale_kernel, dim3(head_copy_blocks(w_copy.n_vec)), 256, 0, st, w_copy);
-      if (err != cudaSuccess) return err;
-    }
+    const HeadExact exact{p.T, p.D, p.h, p.W, en, G, w.ldg, v0, n};
+    err = run_head_exact(exact, dh != nullptr && beside ? &w_copy : nullptr, st);
+    if (err != cudaSuccess) return err;
     if (dh != nullptr) {
       TileArgs d{};
       d.status = p.status;

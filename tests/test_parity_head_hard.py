@@ -1,4 +1,5 @@
-"""Single-exit LM-head operators where they can go wrong: peaked rows whose gradient is small."""
+"""Single-exit LM-head operators where they can go wrong: peaked rows whose gradient is a small
+difference."""
 import functools
 
 import numpy as np
@@ -7,7 +8,7 @@ import torch
 
 from lm_head_loss_junction_b200 import token_logprobs, token_logprobs_bwd, topk_distill_bwd, topk_distill_fwd
 from oracle import head as oh
-from tests.head_helpers import Bounds, half_step, within
+from tests.head_helpers import Bounds, check_grads, half_step, within
 from tests.test_parity_head import gpu
 
 pytestmark = pytest.mark.gpu
@@ -17,13 +18,13 @@ BF, F32 = torch.bfloat16, torch.float32
 
 # ---------------------------------------------------------------- gradients of peaked rows
 @functools.lru_cache(maxsize=None)
-def peaked(T, D, V, seed=0):
+def peaked(T, D, V, dtype=BF, seed=0):
     """Rows that are nearly certain of one token: q_y from 0.99 to 0.9997, and W with a mean row as long as its
     spread, so that what is lost of a row's small probabilities does not average out."""
     rng = np.random.Generator(np.random.PCG64(seed))
     W = rng.normal(size=(V, D)) * 2.0 / np.sqrt(D)
     mean = rng.normal(size=D) * 2.0 / np.sqrt(D)
-    W = torch.from_numpy((W + mean).astype(np.float32)).to(BF)
+    W = torch.from_numpy((W + mean).astype(np.float32)).to(dtype)
     Wd = W.double().numpy()
     y = rng.choice(V, size=T, replace=False).astype(np.int32)
     h, to = rng.normal(size=(T, D)) * 0.5, Wd[y] - mean
@@ -35,45 +36,108 @@ def peaked(T, D, V, seed=0):
         logq, _ = oh.log_softmax(base + mid[:, None] * lean)
         low = np.exp(logq[np.arange(T), y]) < target
         lo, hi = np.where(low, mid, lo), np.where(low, hi, mid)
-    return torch.from_numpy((h + lo[:, None] * to).astype(np.float32)).to(BF), W, y
+    return torch.from_numpy((h + lo[:, None] * to).astype(np.float32)).to(dtype), W, y
+
+
+def check_peaked(b, y, s, dh, dW):
+    """Gradients of s_t (log q_y) of peaked rows: every token's dh and every untouched token's dW row keep their own
+    relative precision.
+
+    Bound of an entry of G, dl the error of a logit: an entry of a small probability is off by 2 dl (its logit and its
+    row's log-sum-exp) + 2^-19 (exp, log) of itself, and 2^-11 (fp16; fp32 path: 2^-22); what is lost below fp16's
+    smallest number is 2^-25 of a row stored between 2^13 and 2^15 times its largest coefficient: 2^-38 s.  The
+    target's own entry is formed from its logit in 64 bits and the fp32 log-sum-exp (rounded, exp and log: 2^-24 |lse|
+    and 2^-20 of s), in which the others' terms are off as above.  fp32 inputs: the log-sum-exp comes from fp32 logits
+    but for the target's, which is as exact."""
+    T, V = b.h.shape[0], b.W.shape[0]
+    rows = np.arange(T)
+    logq, lse = oh.log_softmax(b.h @ b.W.T)
+    assert 0.985 < np.exp(logq[rows, y]).min() and np.exp(logq[rows, y]).max() < 0.9999
+    G = np.exp(logq) * s
+    G[rows, y] = 0.0
+    G[rows, y] = -G.sum(axis=1)
+    rel = 2 * b.dl + 2.0 ** -19 + (2.0 ** -11 if b.bf16 else 2.0 ** -22)
+    e = rel[:, None] * np.abs(G) + (2.0 ** -38 * s if b.bf16 else 0.0)
+    e[rows, y] += s * (2.0 ** -24 * np.abs(lse) + 2.0 ** -20)
+    aG = np.abs(G)
+    exp = G @ b.W
+    within(dh, exp, e @ np.abs(b.W) + b._sum(V) * (aG @ np.abs(b.W)) + half_step(dh.dtype) * np.abs(exp), "dh")
+    rare = np.setdiff1d(np.arange(V), y)
+    exp = G.T[rare] @ b.h
+    # h is copied to fp16 over at most twice its largest value: 2^-38 of that below fp16's normal range
+    copy = 2.0 ** -37 * np.abs(b.h).max() * aG.T[rare].sum(axis=1, keepdims=True) if b.bf16 else 0.0
+    within(dW[torch.from_numpy(rare).cuda()], exp, e.T[rare] @ np.abs(b.h) + copy + b._sum(T) * (aG.T[rare] @ np.abs(b.h)) +
+           half_step(F32) * np.abs(exp), "dW of other tokens")
+
+
+def peaked_step(op, y, h, W, **kw):
+    """dh and dW of the mean of -log q_y."""
+    T = y.shape[0]
+    if op == "score":
+        _, stats, _, _ = token_logprobs(y, h, W, **kw)
+        return token_logprobs_bwd(y, h, W, stats, torch.full((T,), -1.0 / T, device="cuda"))
+    z, ids = torch.zeros(T, 1, device="cuda"), y[:, None].contiguous()
+    _, stats = topk_distill_fwd(y, ids, z, h, W)
+    return topk_distill_bwd(y, ids, z, h, W, stats)
 
 
 @pytest.mark.parametrize("T,D,V", [(150, 128, 49152), (520, 192, 33001), (200, 128, 131072)])
 @pytest.mark.parametrize("op", ["score", "distill"])
 def test_gradients_of_peaked_rows(T, D, V, op):
-    """Every token's dh and every untouched token's dW row keep their own relative precision.
-
-    Bound of an entry of G: both passes form the same logits bit for bit here, so with dl the error of a logit
-    (2 dl of a difference) an entry of a small probability is off by 2 dl + 2^-19 (exp, log) of itself and 2^-11
-    (fp16); what is lost below fp16's smallest number is 2^-25 of a row stored between 2^13 and 2^15 times its largest
-    coefficient: 2^-38 s.  The target's own entry is minus the sum of the others, formed from the fp32 log-sum-exp:
-    the others' errors, 2^-24 |lse| and 2^-20 s."""
     h, W, y = peaked(T, D, V)
-    b = Bounds(h, W)
-    rows = np.arange(T)
-    logq, lse = oh.log_softmax(b.h @ b.W.T)
-    assert 0.985 < np.exp(logq[rows, y]).min() and np.exp(logq[rows, y]).max() < 0.9999
+    check_peaked(Bounds(h, W), y, 1.0 / T, *peaked_step(op, *gpu(y, h, W)))
+
+
+@pytest.mark.parametrize("op,T,D,V,dtype,top_k", [
+    ("score", 20, 128, 49152, BF, 0), ("distill", 20, 128, 49152, BF, 0), ("score", 100, 1024, 9000, BF, 0),
+    ("distill", 60, 2304, 6001, BF, 0), ("score", 20, 4352, 6001, BF, 0), ("score", 150, 2304, 6001, BF, 8),
+    ("score", 520, 640, 6001, BF, 1), ("score", 100, 1024, 9000, BF, 33), ("score", 140, 192, 4001, F32, 0),
+    ("distill", 140, 192, 4001, F32, 0), ("score", 140, 192, 4001, F32, 5)])
+def test_peaked_rows_whatever_made_their_statistics(op, T, D, V, dtype, top_k):
+    """Few tokens and alternatives have their log-sum-exp from other sums than the gradient's logits."""
+    h, W, y = peaked(T, D, V, dtype)
+    kw = dict(top_k=top_k) if top_k else {}
+    check_peaked(Bounds(h, W), y, 1.0 / T, *peaked_step(op, *gpu(y, h, W), **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradients_of_some_rows_of_a_batch(dtype):
+    """The statistics of a long batch, the gradients of a few of its rows."""
+    h, W, y = peaked(300, 512, 6001, dtype)
     hg, Wg, yg = gpu(h, W, y)
-    if op == "score":
-        _, stats, _, _ = token_logprobs(yg, hg, Wg)
-        dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, torch.full((T,), -1.0 / T, device="cuda"))
-    else:
-        z = torch.zeros(T, 1, device="cuda")
-        _, stats = topk_distill_fwd(yg, yg[:, None].contiguous(), z, hg, Wg)
-        dh, dW = topk_distill_bwd(yg, yg[:, None].contiguous(), z, hg, Wg, stats)
-    G = np.exp(logq) / T
-    G[rows, y] = 0.0
-    G[rows, y] = -G.sum(axis=1)
-    s = 1.0 / T
-    rel = 2.0 ** -11 + 2 * b.dl + 2.0 ** -19
-    e = rel[:, None] * np.abs(G) + 2.0 ** -38 * s
-    e[rows, y] += s * (2.0 ** -24 * np.abs(lse) + 2.0 ** -20)
-    aG = np.abs(G)
-    exp = G @ b.W
-    within(dh, exp, e @ np.abs(b.W) + (V / 16 + 32) * 2.0 ** -23 * (aG @ np.abs(b.W)) + half_step(BF) * np.abs(exp), "dh")
-    rare = np.setdiff1d(np.arange(V), y)
-    exp = G.T[rare] @ b.h
-    # h is copied to fp16 over at most twice its largest value: 2^-38 of that below fp16's normal range
-    copy = 2.0 ** -37 * np.abs(b.h).max() * aG.T[rare].sum(axis=1, keepdims=True)
-    within(dW[torch.from_numpy(rare).cuda()], exp, e.T[rare] @ np.abs(b.h) + copy +
-           ((T / 16 + 32) * 2.0 ** -23) * (aG.T[rare] @ np.abs(b.h)) + half_step(F32) * np.abs(exp), "dW of other tokens")
+    _, stats, _, _ = token_logprobs(yg, hg, Wg)
+    for a, b in ((0, 40), (40, 300)):
+        n = b - a
+        dh, dW = token_logprobs_bwd(yg[a:b], hg[a:b], Wg, stats[:, a:b].contiguous(),
+                                    torch.full((n,), -1.0 / n, device="cuda"))
+        check_peaked(Bounds(h[a:b], W), y[a:b], 1.0 / n, dh, dW)
+
+
+def test_heavy_entries_named_twice():
+    """A token that holds its row, named in several places of its list and among the teacher's: its terms count once
+    in the log-sum-exp, its coefficients all of them in the gradient."""
+    T, D, V, K = 40, 1024, 5000, 64
+    h, W, y = peaked(T, D, V)
+    rng = np.random.Generator(np.random.PCG64(2))
+    ids = rng.integers(0, V, size=(T, K)).astype(np.int32)
+    for j in (0, 5, 31, 32, 40, 63):
+        ids[:, j] = np.where(rng.random(T) < 0.7, y, ids[:, j])
+    g = rng.normal(size=(T, K)).astype(np.float32)
+    hg, Wg, ig, gg, yg = gpu(h, W, ids, g, y)
+    b = Bounds(h, W)
+    r = oh.token_logprobs(ids, h, W)
+    logp, stats, _, _ = token_logprobs(ig, hg, Wg)
+    within(stats[0], r["lse"], b.lse(r["lse"]), "lse")
+    within(logp, r["logp"], b.logp(r["lse"])[:, None] * np.ones((1, K)), "logp")
+    once, stats1, _, _ = token_logprobs(yg, hg, Wg)
+    named = torch.from_numpy((ids == y[:, None]).any(axis=1)).cuda()
+    assert torch.equal(stats[:, named], stats1[:, named])
+    dh, dW = token_logprobs_bwd(ig, hg, Wg, stats, gg)
+    s = np.maximum(np.abs(g.astype(np.float64).sum(1)), np.abs(g).max(1))
+    check_grads(b, oh.token_logprobs_grad(ids, h, W, g), s, dh, dW)
+    z = rng.normal(size=(T, K)).astype(np.float32)
+    losses, dstats = topk_distill_fwd(yg, ig, gpu(z)[0], hg, Wg, 0.4)
+    d = oh.topk_distill(y, ids, z, h, W, 0.4)
+    within(dstats[1], d["stats"][1], b.logp(r["lse"]), "ce")
+    within(dstats[2], d["stats"][2], b.logp(r["lse"]) + 2.0 ** -20 * np.abs(d["stats"][2]), "kd")
+    check_grads(b, d["G"], np.full(T, 1.0 / T), *topk_distill_bwd(yg, ig, gpu(z)[0], hg, Wg, dstats, 0.4))
