@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const HeadEntriesIn i
         // a power of two above s |h| (a row of zeros, or of nothing that is a number, counts as 1)
         h_most = warp_max(h_most);
         if (lane == 0 && scale > 0.f) {
-          int e = ilogbf(scale) + (h_most > 0.f && h_most <= 3.4e38f ? ilogbf(h_most) + 1 : 0);
-          e = e < -126 ? -126 : (e > 126 ? 126 : e);
+          // at least 2^-111 s: s over it, times the lift of the copy (2^14), stays in range for subnormal h too
+          const int h_exp = h_most > 0.f && h_most <= 3.4e38f ? max(ilogbf(h_most) + 1, -111) : 0;
+          const int e = min(max(ilogbf(scale) + h_exp, -126), 126);
           atomicMax(out.smax, __float_as_uint(ldexpf(1.f, e)));
         }
       }

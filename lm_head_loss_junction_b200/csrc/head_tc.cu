@@ -230,6 +230,16 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Two powers of two a and s as the factors of a s, each about its root: a sum
+// times a alone, or a s itself, may be out of fp32's range where sum a s is not.
+__device__ __forceinline__ void split_scale(float a, float s, float& f1, float& f2) {
+  f1 = f2 = 0.f;
+  if (!(s > 0.f)) return;
+  const int e = ilogbf(a) + ilogbf(s), half = e / 2;
+  f1 = ldexpf(1.f, half);
+  f2 = ldexpf(1.f, e - half);
+}
+
 // A_MN / B_MN: the operand is stored with its M / N dimension contiguous
 // (boxes of 64 x 64), otherwise with K contiguous.
 template <Epi EPI>
@@ -371,11 +381,14 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
       store_pairs(stage, lane, w, dst + c * 64, a.ld * 2, left_rows);
     }
   } else {
-    const float alpha = EPI == kDw ? __uint_as_float(*a.smax) / kRowLift : *a.inv;
+    // the operands' scales taken out: of the copy of h, or of the copy of W and the row of G'
+    float f1, f2 = 1.f;
+    if constexpr (EPI == kDw) f1 = __uint_as_float(*a.smax) / kRowLift;
+    else split_scale(*a.inv, valid ? a.row[row].w : 0.f, f1, f2);
+    const auto scaled = [&](float v) { return EPI == kDw ? v * f1 : v * f1 * f2; };
     uint8_t* stage = s.stage[warp - 2];
     const int64_t row0 = row - lane;
     if (OUT_BF16 && (EPI == kDw || a.acc == nullptr)) {
-      const float f = EPI == kDh && valid ? a.row[row].w : 1.f;     // apart from alpha: their product can underflow
       const int64_t piece_row = row0 + (lane >> 2);
       uint8_t* dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + piece_row * a.cols + c0 + (lane & 3) * 8);
 #pragma unroll 1
@@ -386,50 +399,47 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
         if (c0 + c * 32 >= a.cols) continue;
         uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(r[2 * k] * alpha * f, r[2 * k + 1] * alpha * f);
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(scaled(r[2 * k]), scaled(r[2 * k + 1]));
         store_pairs(stage, lane, w, dst + c * 64, static_cast<int64_t>(a.cols) * 2, a.rows - piece_row);
       }
-      return;
-    }
-    // fp32 out, or earlier chunks' sums to add before the rounding: fp32 through the staging rows
-    const float rs = EPI == kDh && valid ? a.row[row].w : 1.f;
+    } else if constexpr (!(OUT_BF16 && EPI == kDw)) {
+      // fp32 out, or earlier chunks' sums to add before the rounding: fp32 through the staging rows
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float r[32];
-      tmem_ld32(acc_col + c * 32, r);
-      if (c == 3) release();
-      const int col = c0 + c * 32;
-      if (col >= a.cols) continue;
+      for (int c = 0; c < 4; ++c) {
+        float r[32];
+        tmem_ld32(acc_col + c * 32, r);
+        if (c == 3) release();
+        const int col = c0 + c * 32;
+        if (col >= a.cols) continue;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) r[k] *= alpha;
-      stage_row(stage, lane, r);
-      __syncwarp();
+        for (int k = 0; k < 32; ++k) r[k] = scaled(r[k]);
+        stage_row(stage, lane, r);
+        __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + (lane >> 3), ch = lane & 7;
-        const float scale = __shfl_sync(0xffffffffu, rs, rr);
-        if (row0 + rr >= a.rows) continue;
-        float4 v = *staged(stage, rr, ch);
-        const int64_t off = (row0 + rr) * a.cols + col + ch * 4;
-        if constexpr (OUT_BF16) {
-          const float4 o = *reinterpret_cast<const float4*>(a.acc + off);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off) =
-              make_uint2(pack_bf16x2((v.x + o.x) * scale, (v.y + o.y) * scale),
-                         pack_bf16x2((v.z + o.z) * scale, (v.w + o.w) * scale));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
-                                                  static_cast<int64_t>(part) * a.rows * a.cols + off);
-          if (a.accumulate) {
-            const float4 o = *dst;
-            v.x += o.x;
-            v.y += o.y;
-            v.z += o.z;
-            v.w += o.w;
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+          if (row0 + rr >= a.rows) continue;
+          float4 v = *staged(stage, rr, ch);
+          const int64_t off = (row0 + rr) * a.cols + col + ch * 4;
+          if constexpr (OUT_BF16) {
+            const float4 o = *reinterpret_cast<const float4*>(a.acc + off);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + off) =
+                make_uint2(pack_bf16x2(v.x + o.x, v.y + o.y), pack_bf16x2(v.z + o.z, v.w + o.w));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) +
+                                                    static_cast<int64_t>(part) * a.rows * a.cols + off);
+            if (a.accumulate) {
+              const float4 o = *dst;
+              v.x += o.x;
+              v.y += o.y;
+              v.z += o.z;
+              v.w += o.w;
+            }
+            *dst = v;
           }
-          *dst = v;
         }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
 }
@@ -597,15 +607,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<EPI>(), 1
 }
 
 // dh from the parts of a split K, summed in order: into acc, or with acc (may
-// be NULL) times the row's scale to bf16.
+// be NULL) to bf16.
 struct ReduceArgs {
   const float4* part;              // [parts][n] of four values
   int parts;
   int64_t n;
-  int vec_per_row;
   float4* acc;
   int acc_in;                      // acc holds earlier chunks
-  const float4* row;
   uint2* out;                      // bf16, or NULL: the sums go to acc
 };
 
@@ -641,8 +649,7 @@ __global__ void __launch_bounds__(256) head_reduce_kernel(const ReduceArgs a) {
     a.acc[i] = v;
     return;
   }
-  const float s = a.row[i / a.vec_per_row].w;
-  a.out[i] = make_uint2(pack_bf16x2(v.x * s, v.y * s), pack_bf16x2(v.z * s, v.w * s));
+  a.out[i] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // ------------------------------------------------------------------ host side
@@ -924,10 +931,8 @@ cudaError_t head_tc_backward(const HeadProblem& p, const HeadEntriesIn& in, cons
         const int kb = tiles_of(n, kBK);
         r.parts = tiles_of(kb, tiles_of(kb, w.parts));
         r.n = p.T * p.D / 4;
-        r.vec_per_row = static_cast<int>(p.D / 4);
         r.acc = reinterpret_cast<float4*>(acc);
         r.acc_in = first ? 0 : 1;
-        r.row = en.row;
         r.out = last ? static_cast<uint2*>(dh) : nullptr;
         err = head_launch(head_reduce_kernel, dim3(static_cast<unsigned>((r.n * kReduceLanes + 255) / 256)), 256, 0, st,
                           r);

@@ -8,7 +8,7 @@ import torch
 
 from lm_head_loss_junction_b200 import token_logprobs, token_logprobs_bwd, topk_distill_bwd, topk_distill_fwd
 from oracle import head as oh
-from tests.head_helpers import Bounds, check_grads, half_step, within
+from tests.head_helpers import Bounds, check_grads, half_step, make, within
 from tests.test_parity_head import gpu
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,29 @@ def test_heavy_entries_named_twice():
     within(dstats[1], d["stats"][1], b.logp(r["lse"]), "ce")
     within(dstats[2], d["stats"][2], b.logp(r["lse"]) + 2.0 ** -20 * np.abs(d["stats"][2]), "kd")
     check_grads(b, d["G"], np.full(T, 1.0 / T), *topk_distill_bwd(yg, ig, gpu(z)[0], hg, Wg, dstats, 0.4))
+
+
+# ---------------------------------------------------------------- magnitudes
+class Tiny(Bounds):
+    """With what is lost below the smallest normal number: half of the output's smallest number, and of fp32's for
+    each part of a sum (at most 74, and the copies')."""
+
+    def dh(self, G, s, out):
+        return super().dh(G, s, out) + torch.finfo(out).smallest_normal * torch.finfo(out).eps / 2 + 80 * 2.0 ** -150
+
+    def dW(self, G, s, out):
+        return super().dW(G, s, out) + torch.finfo(out).smallest_normal * torch.finfo(out).eps / 2 + 80 * 2.0 ** -150
+
+
+@pytest.mark.parametrize("T", [20, 600])
+@pytest.mark.parametrize("shift", [-114, -100, 114, 118])
+def test_magnitudes_near_the_ends_of_bf16(T, shift):
+    """W times 2^shift and h times 2^-shift; gradients within the bounds of any magnitude."""
+    _, h, W, y = make(T, 64, 700, BF, seed=14)
+    h, W = torch.ldexp(h.float(), torch.tensor(-shift)).to(BF), torch.ldexp(W.float(), torch.tensor(shift)).to(BF)
+    yg, hg, Wg = gpu(y, h, W)
+    _, stats, _, _ = token_logprobs(yg, hg, Wg)
+    for g in (1.0, 2.0 ** -20):
+        dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, torch.full((T,), g, device="cuda"))
+        assert torch.isfinite(dh).all() and torch.isfinite(dW).all()
+        check_grads(Tiny(h, W), oh.token_logprobs_grad(y[:, None], h, W, np.full((T, 1), g)), np.full(T, g), dh, dW)
