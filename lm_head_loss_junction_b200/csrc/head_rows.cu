@@ -248,7 +248,11 @@ __global__ void __launch_bounds__(256) head_exact_kernel(const HeadExact x, unsi
 // (m, z, u) of two column sets -> of their union.
 __device__ __forceinline__ void merge_part(float& m, float& z, float& u, float m2, float z2, float u2) {
   const float top = fmaxf(m, m2);
-  if (!(top > -INFINITY)) return;                        // nothing on either side (or NaN below)
+  if (!(top > -INFINITY)) {                              // nothing on either side, or nothing that is a number
+    z += z2;
+    u += u2;
+    return;
+  }
   if (z > 0.f || z != z) {
     const float d = m - top, f = ex2(d);
     u = f * fmaf(d, z, u);

@@ -167,3 +167,20 @@ def test_magnitudes_near_the_ends_of_bf16(T, shift):
         dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, torch.full((T,), g, device="cuda"))
         assert torch.isfinite(dh).all() and torch.isfinite(dW).all()
         check_grads(Tiny(h, W), oh.token_logprobs_grad(y[:, None], h, W, np.full((T, 1), g)), np.full(T, g), dh, dW)
+
+
+# ---------------------------------------------------------------- rows that are not numbers
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("V", [5, 128, 1024])
+def test_rows_that_are_not_numbers_have_no_statistics(dtype, T, V):
+    """NaN, not minus infinity, whether or not the vocabulary fills its last block of columns."""
+    _, h, W, y = make(T, 64, V, dtype, seed=26)
+    h[T // 2] = float("nan")
+    hg, Wg, yg = gpu(h, W, y)
+    for K in (0, 3):
+        logp, stats, _, _ = token_logprobs(yg, hg, Wg, top_k=K)
+        assert torch.isnan(stats[:, T // 2]).all() and torch.isnan(logp[T // 2])
+        assert torch.isfinite(stats).sum() == 2 * (T - 1) and torch.isfinite(logp).sum() == T - 1
+    _, stats = topk_distill_fwd(yg, yg[:, None].contiguous(), torch.zeros(T, 1, device="cuda"), hg, Wg)
+    assert torch.isnan(stats[:, T // 2]).all()
