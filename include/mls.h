@@ -499,7 +499,9 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  *   top_ids    device int32 [T, K]: the K largest logits, largest first, equal
  *              ones by ascending id.  The order is that of the products summed
  *              in 64 bits, so it does not depend on T, the workspace or the
- *              position.  -1 (and NaN) where fewer than K logits are numbers.
+ *              position.  A logit that is not a number is no alternative (the
+ *              log probabilities of its row are NaN): -1 (and NaN) where fewer
+ *              than K are numbers.
  *   top_logp   device f32 [T, K]: their log probabilities
  * Without alternatives and past 128 tokens MLS_BF16 never writes the logits;
  * otherwise those of one block of tokens at a time go to the workspace in fp32.

@@ -497,6 +497,8 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
 // a logit past it can be dropped too.  What is left (a few more than C) is
 // ranked by counting.  Where the border is past the bins or too much is left
 // (equal logits), radix selection over the whole row takes the place of it.
+// A logit that is not a number is passed over everywhere (its key, where it has
+// one, lies below that of -infinity).
 //
 // The candidates are then ranked by their products again, so that the ids do
 // not depend on the tile a token fell into (4 more than K: a logit whose fp32
@@ -746,7 +748,8 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   if (n_splits >= C) {
     for (int i = threadIdx.x; i < n_splits; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, maxima[i])], 1);
   } else {
-    for (int i = threadIdx.x; i < f.V; i += kTopThreads) atomicAdd(&s.hist[bin_of(largest, row[i])], 1);
+    for (int i = threadIdx.x; i < f.V; i += kTopThreads)
+      if (row[i] == row[i]) atomicAdd(&s.hist[bin_of(largest, row[i])], 1);
   }
   __syncthreads();
   if (warp == 0) {
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (col + k >= f.V || bin_of(largest, v[k]) > border) continue;
+      if (col + k >= f.V || v[k] != v[k] || bin_of(largest, v[k]) > border) continue;
       const int at = atomicAdd(&s.count, 1);
       if (at < list) keys[at] = top_key(v[k], static_cast<uint32_t>(col + k));
     }
@@ -794,13 +797,16 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   int n = s.count;
   if (n > list) {
     // keys made from the logits on every pass; C of them are at or above the C-th
-    const auto at = [&](int i) { return top_key(row[i], static_cast<uint32_t>(i)); };
+    const auto at = [&](int i) {
+      const float v = row[i];
+      return v == v ? top_key(v, static_cast<uint32_t>(i)) : static_cast<uint64_t>(~static_cast<uint32_t>(i));
+    };
     const uint64_t last = select_kth<kTopThreads>(at, static_cast<int>(f.V), C, s.hist, s.chosen);
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < f.V; i += kTopThreads) {
       const uint64_t key = at(i);
-      if (key >= last) keys[atomicAdd(&s.count, 1)] = key;
+      if (key >= last && key >> 32 != 0) keys[atomicAdd(&s.count, 1)] = key;
     }
     __syncthreads();
     n = s.count;

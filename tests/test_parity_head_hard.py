@@ -184,3 +184,32 @@ def test_rows_that_are_not_numbers_have_no_statistics(dtype, T, V):
         assert torch.isfinite(stats).sum() == 2 * (T - 1) and torch.isfinite(logp).sum() == T - 1
     _, stats = topk_distill_fwd(yg, yg[:, None].contiguous(), torch.zeros(T, 1, device="cuda"), hg, Wg)
     assert torch.isnan(stats[:, T // 2]).all()
+
+
+# ---------------------------------------------------------------- alternatives
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("V,K", [(5, 5), (90, 64), (3000, 20), (3000, 64), (130, 64)])
+@pytest.mark.parametrize("spread", [1.0, 8.0])
+def test_logits_that_are_not_numbers_are_no_alternatives(dtype, T, V, K, spread):
+    """The K largest of those that are, then -1 and NaN."""
+    rng, h, W, _ = make(T, 64, V, dtype, seed=23)
+    h = (h.float() * spread).to(dtype)
+    gone = np.zeros(V, dtype=bool)
+    gone[rng.choice(V, size=3 if V < 3000 else 400, replace=False)] = True
+    if V == 130:
+        gone[5:120] = True
+    if V == 3000:
+        gone[256:512] = True                              # whole splits
+    W[torch.from_numpy(gone)] = float("nan")
+    hg, Wg = gpu(h, W)
+    hg = torch.cat([hg, torch.full_like(hg[:1], float("nan"))])
+    _, stats, top, top_logp = token_logprobs(None, hg, Wg, top_k=K)
+    l = oh.head_logits(h, W)
+    l[:, gone] = -np.inf
+    order = np.argsort(-l, axis=1, kind="stable")[:, :K]
+    have = min(K, int((~gone).sum()))
+    order[:, have:] = -1
+    np.testing.assert_array_equal(top.cpu().numpy()[:T], order)
+    assert (top[T] == -1).all()                           # a row that is no number has none
+    assert torch.isnan(top_logp).all() and torch.isnan(stats).all()
