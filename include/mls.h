@@ -498,10 +498,15 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  *              K > 0; N + K >= 1
  *   top_ids    device int32 [T, K]: the K largest logits, largest first, equal
  *              ones by ascending id.  The order is that of the products summed
- *              in 64 bits, so it does not depend on T, the workspace or the
- *              position.  A logit that is not a number is no alternative (the
- *              log probabilities of its row are NaN): -1 (and NaN) where fewer
- *              than K are numbers.
+ *              in 64 bits, of all logits that their fp32 sums leave in doubt, so it
+ *              does not depend on T, the workspace or the position; two cases are
+ *              left to the fp32 sums: more than 640 logits in doubt about the
+ *              K-th, and a row of W more than twice as long as any of the K + 4
+ *              largest logits' that is in doubt by its length alone.  "In doubt":
+ *              nearer to the K-th than (D / 16 + 40) 2^-22 |h| |W_v|, the largest
+ *              |W_v| of those (MLS_F32: D / 2).  A logit that is not a number is
+ *              no alternative (the log probabilities of its row are NaN): -1 (and
+ *              NaN) where fewer than K are numbers.
  *   top_logp   device f32 [T, K]: their log probabilities
  * Without alternatives and past 128 tokens MLS_BF16 never writes the logits;
  * otherwise those of one block of tokens at a time go to the workspace in fp32.

@@ -21,10 +21,11 @@
 namespace mls {
 
 // Products h . W[id[g]] in 64 bits of G rows of W at once (their loads in
-// flight together), by one warp; lane 0's results count.
+// flight together), by one warp, each lane with the results.  w2 (fp32 inputs,
+// may be NULL): the rows' squared norms.
 template <bool BF16, int G>
 __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, const int* id, int lane,
-                                       double (&acc)[G]) {
+                                       double (&acc)[G], float* w2 = nullptr) {
 #pragma unroll
   for (int g = 0; g < G; ++g) acc[g] = 0.0;
   if constexpr (BF16) {
@@ -51,10 +52,21 @@ __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, 
     }
   } else {
     const float* a = static_cast<const float*>(h);
+    float sq[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sq[g] = 0.f;
     for (int64_t i = lane; i < D; i += 32) {
       const double x = a[i];
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = fma(x, static_cast<double>(static_cast<const float*>(W)[id[g] * D + i]), acc[g]);
+      for (int g = 0; g < G; ++g) {
+        const float w = static_cast<const float*>(W)[id[g] * D + i];
+        acc[g] = fma(x, static_cast<double>(w), acc[g]);
+        sq[g] = fmaf(w, w, sq[g]);
+      }
+    }
+    if (w2 != nullptr) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) w2[g] = warp_sum(sq[g]);
     }
   }
 #pragma unroll

@@ -501,13 +501,20 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
 // one, lies below that of -infinity).
 //
 // The candidates are then ranked by their products again, so that the ids do
-// not depend on the tile a token fell into (4 more than K: a logit whose fp32
-// value misplaces it by the border is among them).  First with fp32 sums of 8
+// not depend on the tile a token fell into.  First with fp32 sums of 8
 // products, added in 64 bits: each such sum is off by at most 7 half units of
 // sum |h_i w_i|, a whole product by 7 2^-24 |h| |w| (Cauchy-Schwarz).  Where two
 // neighbours among the first K + 1 are nearer than twice that, the token's
 // candidates are multiplied once more with every product exact and added in 64
 // bits; then only equal logits tie, and the lower id comes first.
+//
+// That is the order of all logits if none that was left out can reach the K-th:
+// the last candidate's fp32 logit, and so every one left out, lies below the
+// K-th's product by more than an fp32 logit can be off.  Four candidates more
+// than K make that so for nearly every row (K = 32 of 49152 columns at D = 2304:
+// a bound of 0.004 for logits that spread by 2, the gap of four places 0.06).
+// Elsewhere (rows of W that differ in their last bits) every logit that can
+// reach it, up to kWide of them, is multiplied exactly and ranked.
 //
 // The candidates' terms of z and u, the ones that weigh, are replaced by those
 // of these products, which are more exact than the tensor cores' sums, and so
@@ -649,25 +656,32 @@ __device__ __forceinline__ void block_dots_fast(const void* h, const void* W, in
   }
 }
 
-// val[i] = h . W[id[i]] for i < n, by the block's warps.
+// val[i] = h . W[id[i]] for i < n, by the block's warps; norm (fp32 inputs, may be NULL): as above.
 template <bool BF16, int G>
 __device__ __forceinline__ void block_dots(const void* h, const void* W, int64_t D, const int* id, int n, double* val,
-                                           int warp, int warps, int lane) {
+                                           int warp, int warps, int lane, unsigned int* norm = nullptr) {
   for (int i = warp * G; i < n; i += warps * G) {
     int own[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) own[g] = id[i + g < n ? i + g : n - 1];
     double acc[G];
-    dots64<BF16, G>(h, W, D, own, lane, acc);
+    float w2[G];
+    dots64<BF16, G>(h, W, D, own, lane, acc, norm != nullptr ? w2 : nullptr);
     if (lane == 0) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        if (i + g < n) val[i + g] = acc[g];
+        if (i + g < n) {
+          val[i + g] = acc[g];
+          if (norm != nullptr) atomicMax(norm, __float_as_uint(w2[g]));
+        }
     }
   }
 }
 
 constexpr int kBins = 256;
+constexpr int kTopList = 1024;             // logits that the selection may leave, as keys
+constexpr int kWide = 640;                 // logits about the K-th that are ranked exactly, in the same memory
+static_assert(kWide * (sizeof(double) + sizeof(int)) <= kTopList * sizeof(uint64_t), "room");
 constexpr int kTopSmemLimit = 200 * 1024;
 
 struct TopSmem {
@@ -676,6 +690,7 @@ struct TopSmem {
   float part[32][2];                         // sums z and u of each warp's splits
   float h2;
   unsigned int w2;                           // largest squared norm of a candidate's row, as bits
+  double kth;                                // product of the K-th, where the candidates were ranked again
   int count, n_sel, border;
   int given[kMaxEntries];                    // the given tokens' ids
   int id[2 * kMaxEntries + kTopMore];        // rows to multiply: the given tokens, then the candidates by rank
@@ -691,12 +706,12 @@ __device__ __forceinline__ int bin_of(float largest, float v) {
 }
 
 template <bool BF16, int kTopThreads>
-__global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C, int list) {
+__global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish f, int C) {
   constexpr int kWarps = kTopThreads / 32;
   extern __shared__ __align__(16) uint8_t raw[];
   TopSmem& s = *reinterpret_cast<TopSmem*>(raw);
-  uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);   // [list]
-  float* maxima = reinterpret_cast<float*>(keys + list);                                  // [n_splits]
+  uint64_t* keys = reinterpret_cast<uint64_t*>(raw + (sizeof(TopSmem) + 15) / 16 * 16);   // [kTopList]
+  float* maxima = reinterpret_cast<float*>(keys + kTopList);                              // [n_splits]
   int* sel = reinterpret_cast<int*>(maxima + f.n_splits);                                 // [n_splits]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = blockIdx.x;
@@ -790,12 +805,12 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     for (int k = 0; k < 4; ++k) {
       if (col + k >= f.V || v[k] != v[k] || bin_of(largest, v[k]) > border) continue;
       const int at = atomicAdd(&s.count, 1);
-      if (at < list) keys[at] = top_key(v[k], static_cast<uint32_t>(col + k));
+      if (at < kTopList) keys[at] = top_key(v[k], static_cast<uint32_t>(col + k));
     }
   }
   __syncthreads();
   int n = s.count;
-  if (n > list) {
+  if (n > kTopList) {
     // keys made from the logits on every pass; C of them are at or above the C-th
     const auto at = [&](int i) {
       const float v = row[i];
@@ -811,7 +826,7 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
     __syncthreads();
     n = s.count;
   }
-  const int have = n < C ? n : C;                        // fewer only where logits are not numbers
+  int have = n < C ? n : C;                              // fewer only where logits are not numbers
   for (int i = threadIdx.x; i < n; i += kTopThreads) {
     const uint64_t key = keys[i];
     int rank = 0;
@@ -827,45 +842,54 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   // the given tokens' and the candidates' logits as products
   const char* hrow = static_cast<const char*>(f.h) + t * f.D * (BF16 ? 2 : 4);
   const int items = f.N + have;
-  if constexpr (BF16) {
-    if (warp == kWarps - 1) {
-      // |h|^2, for the bound on the sums' error
-      float h2 = 0.f;
+  if (warp == kWarps - 1) {
+    // |h|^2, for the bounds on the sums' errors
+    float h2 = 0.f;
+    if constexpr (BF16) {
       for (int i = lane; i < f.D / 8; i += 32) {
         float x[8];
         bf16x8_to_f32(reinterpret_cast<const uint4*>(hrow)[i], x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h2 = fmaf(x[k], x[k], h2);
       }
-      h2 = warp_sum(h2);
-      if (lane == 0) s.h2 = h2;
+    } else {
+      for (int64_t i = lane; i < f.D; i += 32) {
+        const float x = reinterpret_cast<const float*>(hrow)[i];
+        h2 = fmaf(x, x, h2);
+      }
     }
+    h2 = warp_sum(h2);
+    if (lane == 0) s.h2 = h2;
+  }
+  if constexpr (BF16) {
     if (items <= kWarps) block_dots_fast<1>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
     else if (items <= 3 * kWarps) block_dots_fast<3>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
     else block_dots_fast<5>(hrow, f.W, f.D, s.id, items, s.fine, &s.w2, warp, kWarps, lane);
   } else {
-    block_dots<false, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane);
+    block_dots<false, 3>(hrow, f.W, f.D, s.id, items, s.fine, warp, kWarps, lane, &s.w2);
   }
   __syncthreads();
   // still in that order, no two of the first K + 1 nearer than the error, none of the rest among the first K?
   const int r = threadIdx.x;
   const double* fine = s.fine + f.N;
+  const float unit = 5.9604645e-8f * sqrtf(s.h2) * sqrtf(__uint_as_float(s.w2));   // 2^-24 of the largest |h| |w|
   bool keep = true;
   if ((r + 1 < have && r < f.K) || (r > f.K && r < have)) {
     double off = 0.0;                                    // fp32 inputs: these products are the exact ones
-    if constexpr (BF16) off = 2.f * 8.f * 5.9604645e-8f * sqrtf(s.h2) * sqrtf(__uint_as_float(s.w2));   // 7, and the norms' rounding
+    if constexpr (BF16) off = 2.f * 8.f * unit;          // 7, and the norms' rounding
     keep = (r < f.K ? fine[r] - fine[r + 1] : fine[f.K - 1] - fine[r]) > off;
   }
   if (r < have) s.rank[r] = r;
-  if (__syncthreads_or(!keep)) {
+  // doubles as ordered integers, so that every value (a NaN too) has one rank
+  const auto order = [](double d) {
+    const int64_t b = __double_as_longlong(d + 0.0);
+    return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
+  };
+  const bool again = __syncthreads_or(!keep);
+  if (again) {
     if constexpr (BF16) block_dots<true, 3>(hrow, f.W, f.D, s.id + f.N, have, s.fine + f.N, warp, kWarps, lane);
     __syncthreads();
     if (r < have) {
-      // doubles as ordered integers, so that every value (a NaN too) has one rank
-      const auto order = [](double d) {
-        const int64_t b = __double_as_longlong(d + 0.0);
-        return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (uint64_t(1) << 63);
-      };
       const uint64_t mine = order(fine[r]);
       int rank = 0;
       for (int i = 0; i < have; ++i) {
@@ -873,6 +897,47 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
         rank += other > mine || (other == mine && s.id[f.N + i] < s.id[f.N + r]);
       }
       s.rank[r] = rank;
+      if (rank == f.K - 1) s.kth = fine[r];
+    }
+    __syncthreads();
+  }
+  if (have == C && C < f.V) {
+    // A logit of the row is off by at most D / 16 truncated sums (2^-23 of sum |h_i w_i| each; fp32: D rounded ones, half
+    // of that each) and some 32 more, for rows of W up to twice as long as the candidates' longest.
+    const double kth = again ? s.kth : fine[f.K - 1];
+    const double least = kth - 4.0 * (static_cast<double>(f.D) * (BF16 ? 1.0 / 16 : 0.5) + 40.0) * unit;
+    if (unit != 0.f && !(s.tile[C - 1] < least)) {
+      double* val = reinterpret_cast<double*>(keys);     // [kWide]
+      int* id = reinterpret_cast<int*>(val + kWide);     // [kWide]
+      if (threadIdx.x == 0) s.count = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < f.V; i += kTopThreads) {
+        const float v = row[i];
+        if (v != v || v < least) continue;
+        const int at = atomicAdd(&s.count, 1);
+        if (at < kWide) id[at] = i;
+      }
+      __syncthreads();
+      const int wide = s.count;
+      if (wide <= kWide) {
+        block_dots<BF16, 3>(hrow, f.W, f.D, id, wide, val, warp, kWarps, lane);
+        __syncthreads();
+        have = min(wide, C);
+        for (int i = threadIdx.x; i < wide; i += kTopThreads) {
+          const uint64_t mine = order(val[i]);
+          int rank = 0;
+          for (int j = 0; j < wide; ++j) {
+            const uint64_t other = order(val[j]);
+            rank += other > mine || (other == mine && id[j] < id[i]);
+          }
+          if (rank >= have) continue;
+          s.id[f.N + rank] = id[i];
+          s.fine[f.N + rank] = val[i];
+          s.tile[rank] = row[id[i]];
+          s.rank[rank] = rank;
+        }
+        __syncthreads();
+      }
     }
   }
   const int rank = r < have ? s.rank[r] : 0;
@@ -957,11 +1022,7 @@ cudaError_t run_head_finish(const HeadFinish& f, cudaStream_t st) {
 
 cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   const int C = static_cast<int>(f.V < f.K + kTopMore ? f.V : f.K + kTopMore);
-  // room for what the selection leaves: usually little more than C; the whole of a short row; never less than C
-  const int64_t padded = (f.V + 1) / 2 * 2;
-  const int list = padded < 1024 ? static_cast<int>(padded) : 1024;
-  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + static_cast<size_t>(list) * sizeof(uint64_t) +
-                      static_cast<size_t>(f.n_splits) * 8;
+  const size_t smem = (sizeof(TopSmem) + 15) / 16 * 16 + kTopList * sizeof(uint64_t) + static_cast<size_t>(f.n_splits) * 8;
   // Few tokens leave SMs idle: their blocks get the warps that help, one per product (T = 1, D = 2304, K = 8: the whole
   // call 50.2 us with 512 threads, 51.4 with 1024; T = 24, D = 1024, K = 20: 34.6 and 32.6).
   // Of many tokens small blocks are best, more of them in flight per SM, until the products outweigh the steps before
@@ -979,7 +1040,7 @@ cudaError_t run_head_top(const HeadFinish& f, cudaStream_t st) {
   // the limit is the same on every call: another host thread's call may set it between here and the launch
   const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmemLimit);
   if (err != cudaSuccess) return err;
-  return head_launch(fn, dim3(static_cast<unsigned>(f.T)), threads, smem, st, f, C, list);
+  return head_launch(fn, dim3(static_cast<unsigned>(f.T)), threads, smem, st, f, C);
 }
 
 }  // namespace mls

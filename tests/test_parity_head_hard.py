@@ -1,5 +1,5 @@
 """Single-exit LM-head operators where they can go wrong: peaked rows whose gradient is a small
-difference."""
+difference, magnitudes near the ends of the type, logits that are not numbers, alternatives that differ in the last bits."""
 import functools
 
 import numpy as np
@@ -8,7 +8,7 @@ import torch
 
 from lm_head_loss_junction_b200 import token_logprobs, token_logprobs_bwd, topk_distill_bwd, topk_distill_fwd
 from oracle import head as oh
-from tests.head_helpers import Bounds, check_grads, half_step, make, within
+from tests.head_helpers import Bounds, check_grads, check_top, half_step, make, within
 from tests.test_parity_head import gpu
 
 pytestmark = pytest.mark.gpu
@@ -213,3 +213,40 @@ def test_logits_that_are_not_numbers_are_no_alternatives(dtype, T, V, K, spread)
     np.testing.assert_array_equal(top.cpu().numpy()[:T], order)
     assert (top[T] == -1).all()                           # a row that is no number has none
     assert torch.isnan(top_logp).all() and torch.isnan(stats).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_alternatives_that_differ_in_the_last_bits(dtype, T):
+    """More near-equal logits about the K-th than the fp32 sums can tell apart: the order is that of the products in
+    64 bits, lower ids first where those are equal."""
+    rng = np.random.Generator(np.random.PCG64(21))
+    D, V, n = 512, 5000, 60
+    W = rng.normal(size=(V, D)) * 0.05
+    ids = rng.choice(V, size=n, replace=False)
+    W = torch.from_numpy(W.astype(np.float32)).to(BF)
+    # the same values in other orders: with equal entries of h the sums are equal, the fp32 ones hardly ever
+    row = (np.abs(rng.normal(size=D)) * 2.0 ** rng.uniform(-14, 1, size=D)).astype(np.float32)
+    W[ids] = torch.from_numpy(np.stack([rng.permutation(row) for _ in range(n)])).to(BF)
+    h = torch.from_numpy(np.outer(1.0 + np.arange(T) % 3, np.ones(D)).astype(np.float32)).to(BF)
+    # of one row in two, three entries are a bit off: so are the sums, by the values that meet them
+    h[1::2, :3] = 2.0 ** -7 + h[1::2, :3]
+    h, W = h.to(dtype), W.to(dtype)
+    hg, Wg = gpu(h, W)
+    b, r = Bounds(h, W), oh.token_logprobs(None, h, W)
+    for K in (1, 7, 33, 60, 64):
+        _, stats, top, logp = token_logprobs(None, hg, Wg, top_k=K)
+        check_top(top, logp, h, W, K, b)
+        within(stats[0], r["lse"], b.lse(r["lse"]), "lse")
+        within(stats[1], r["entropy"], b.entropy(r["entropy"]), "entropy")
+
+
+def test_more_logits_in_doubt_than_are_ranked_again():
+    """Equal rows of W past the 640 that are: their fp32 sums are equal too, so the lower ids come first all the same."""
+    rng = np.random.Generator(np.random.PCG64(27))
+    _, h, W, _ = make(50, 128, 3000, BF, seed=27)
+    W[torch.from_numpy(rng.choice(3000, size=900, replace=False))] = (h.float().mean(0) * 2).to(BF)
+    hg, Wg = gpu(h, W)
+    for K in (1, 64):
+        _, _, top, logp = token_logprobs(None, hg, Wg, top_k=K)
+        check_top(top, logp, h, W, K, Bounds(h, W))
