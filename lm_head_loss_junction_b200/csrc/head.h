@@ -39,9 +39,14 @@ typedef float4 HeadPart;
 // 4352, logits of random rows and of a leant-to row alike.  A quarter of 2^-24
 // per step is given back here (D = 2304: the mean error of a logit falls from
 // 2.1e-6 to under 0.2e-6 of it, the root mean square from 4.8e-6 to 2.4e-6;
-// plain fp32 sums have 0.9e-6).  parts: accumulators that share the steps.
+// plain fp32 sums have 0.9e-6).  A row whose sums are exact (a few entries, small
+// whole numbers) was not shrunk and is off by what is given back, so no more is
+// given than was measured: 4352 2^-30 = 4.1e-6 of a logit at most, whatever D.
+// parts: accumulators that share the steps.
+constexpr int64_t kTruncationMeasured = 4352;
 inline float head_log2e(int64_t D, int parts) {
-  return static_cast<float>(1.4426950408889634 * (1.0 + static_cast<double>(D) / parts / 1073741824.0));
+  const int64_t d = D / parts < kTruncationMeasured ? D / parts : kTruncationMeasured;
+  return static_cast<float>(1.4426950408889634 * (1.0 + static_cast<double>(d) / 1073741824.0));
 }
 
 struct HeadProblem {

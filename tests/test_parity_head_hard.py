@@ -250,3 +250,50 @@ def test_more_logits_in_doubt_than_are_ranked_again():
     for K in (1, 64):
         _, _, top, logp = token_logprobs(None, hg, Wg, top_k=K)
         check_top(top, logp, h, W, K, Bounds(h, W))
+
+
+# ---------------------------------------------------------------- widths and exact rows
+@pytest.mark.parametrize("D", [2304, 4352])
+@pytest.mark.parametrize("T", [1, 70, 150])
+def test_the_widths_of_the_larger_exits(D, T):
+    rng, h, W, y = make(T, D, 2000, BF, seed=24)
+    hg, Wg, yg = gpu(h, W, y)
+    b = Bounds(h, W)
+    r = oh.token_logprobs(y[:, None], h, W)
+    logp, stats, _, _ = token_logprobs(yg, hg, Wg)
+    within(stats[0], r["lse"], b.lse(r["lse"]), "lse")
+    within(stats[1], r["entropy"], b.entropy(r["entropy"]), "entropy")
+    within(logp[:, None], r["logp"], b.logp(r["lse"])[:, None], "logp")
+    _, _, top, top_logp = token_logprobs(None, hg, Wg, top_k=20)
+    check_top(top, top_logp, h, W, 20, b)
+    g = rng.normal(size=(T, 1)).astype(np.float32)
+    dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, gpu(g)[0][:, 0].contiguous())
+    check_grads(b, oh.token_logprobs_grad(y[:, None], h, W, g), np.abs(g[:, 0]), dh, dW)
+
+
+@pytest.mark.parametrize("D", [64, 2304, 4352, 65536])
+@pytest.mark.parametrize("T", [1, 128, 129])
+def test_rows_whose_sums_are_exact(D, T):
+    """h with one entry a row, and h and W of small whole numbers: no addition rounds or truncates, so what is left
+    is the correction for truncation that did not happen: at most min(D, 4352) 2^-30 of a logit (the fp32 log-sum-exp and
+    the exponentials: 2^-20 as everywhere)."""
+    rng = np.random.Generator(np.random.PCG64(25))
+    V = 300
+    for kind in ("one", "whole"):
+        W = rng.integers(-8, 9, size=(V, D)) / 4.0
+        h = np.zeros((T, D))
+        if kind == "one":
+            h[np.arange(T), rng.integers(0, D, size=T)] = rng.integers(1, 33, size=T)
+        else:
+            at = rng.integers(0, D, size=(T, 6))
+            h[np.arange(T)[:, None], at] = rng.integers(-3, 4, size=(T, 6))
+        h, W = torch.from_numpy(h).to(BF), torch.from_numpy(W).to(BF)
+        l = oh.head_logits(h, W)
+        logq, lse = oh.log_softmax(l)
+        ids = np.argsort(-l, axis=1, kind="stable")[:, [0, V // 2]].astype(np.int32)
+        hg, Wg, ig = gpu(h, W, ids)
+        logp, stats, _, _ = token_logprobs(ig, hg, Wg)
+        off = min(D, 4352) * 2.0 ** -30 * np.abs(l).max(axis=1) + 2.0 ** -20 * (1 + np.abs(lse))
+        within(stats[0], lse, off, kind + " lse")
+        exp = np.take_along_axis(logq, ids, axis=1)
+        within(logp, exp, (2 * off)[:, None] + 2.0 ** -22 * np.abs(exp), kind + " logp")
