@@ -187,6 +187,24 @@ def test_rows_that_are_not_numbers_have_no_statistics(dtype, T, V):
 
 
 # ---------------------------------------------------------------- alternatives
+@pytest.mark.parametrize("T", [1, 70, 200])
+@pytest.mark.parametrize("spread", [1.0, 2.0, 3.0, 8.0])
+def test_alternatives_of_rows_of_every_spread(T, spread):
+    """From flat rows to rows of which only a handful of logits lie within 16 of the largest."""
+    rng, h, W, y = make(T, 128, 6000, BF, seed=22)
+    h = (h.float() * spread).to(BF)
+    ids = np.stack([y, rng.integers(0, 6000, size=T)], axis=1).astype(np.int32)
+    hg, Wg, ig = gpu(h, W, ids)
+    b = Bounds(h, W)
+    r = oh.token_logprobs(ids, h, W)
+    for K in (2, 64):
+        logp, stats, top, top_logp = token_logprobs(ig, hg, Wg, top_k=K)
+        check_top(top, top_logp, h, W, K, b)
+        within(stats[0], r["lse"], b.lse(r["lse"]), "lse")
+        within(stats[1], r["entropy"], b.entropy(r["entropy"]), "entropy")
+        within(logp, r["logp"], b.logp(r["lse"])[:, None] * np.ones((1, 2)) + 2.0 ** -22 * np.abs(r["logp"]), "logp")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T", [1, 40, 300])
 @pytest.mark.parametrize("V,K", [(5, 5), (90, 64), (3000, 20), (3000, 64), (130, 64)])
