@@ -363,6 +363,15 @@ def _head_workspace(ws, nbytes, dev):
     return ws, ws.numel() * ws.element_size()
 
 
+def _head_status(status, dev):
+    """A word at least: flags would be lost in an empty tensor, or set in what lies behind an empty view."""
+    if status is None:
+        return
+    _head_fit(status, "status", torch.int32, status.shape, dev)
+    if status.numel() == 0:
+        raise ValueError("status must have an element")
+
+
 def _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW):
     if not want_dh and dh is not None or not want_dW and dW is not None:
         raise ValueError("an output was given for a gradient that is not wanted")
@@ -449,8 +458,7 @@ def token_logprobs(ids: Optional[torch.Tensor], h: torch.Tensor, W: torch.Tensor
         _head_fit(top_logp, "top_logp", f32, (T, top_k), dev)
     elif top_k:
         top_logp = torch.empty(T, top_k, dtype=f32, device=dev)
-    if status is not None:
-        _head_fit(status, "status", torch.int32, status.shape, dev)
+    _head_status(status, dev)
     workspace, ws_bytes = _head_workspace(workspace, nbytes, dev)
     check("mls_token_logprobs",
           lib().mls_token_logprobs(T, D, V, N, _ptr(ids), h.data_ptr(), W.data_ptr(), dt, _ptr(logp),
@@ -485,8 +493,7 @@ def token_logprobs_bwd(ids: torch.Tensor, h: torch.Tensor, W: torch.Tensor, stat
     _head_fit(g_logp, "g_logp", torch.float32, ids.shape, dev)
     if g_entropy is not None:
         _head_fit(g_entropy, "g_entropy", torch.float32, (T,), dev)
-    if status is not None:
-        _head_fit(status, "status", torch.int32, status.shape, dev)
+    _head_status(status, dev)
     dh, dW, dW_code = _head_grads(h, W, dh, dW, dW_dtype, accumulate_dW, want_dh, want_dW)
     workspace, ws_bytes = _head_workspace(workspace, token_logprobs_bwd_workspace(T, D, V, N, h.dtype)[0], dev)
     check("mls_token_logprobs_bwd",
@@ -516,8 +523,7 @@ def _distill_common(y, teacher_ids, teacher_logits, token_weights, h, W, status)
     _head_fit(teacher_logits, "teacher_logits", torch.float32, (T, K), dev)
     if token_weights is not None:
         _head_fit(token_weights, "token_weights", torch.float32, (T,), dev)
-    if status is not None:
-        _head_fit(status, "status", torch.int32, status.shape, dev)
+    _head_status(status, dev)
     return T, D, V, K, dt, dev
 
 

@@ -148,3 +148,14 @@ def test_every_workspace_from_the_minimum_up_is_a_valid_size(T, V):
             assert 0 < least <= n
         f, f_min, b, b_min = topk_distill_workspace(T, 64, V, 3, dt)
         assert 0 < f_min <= f and 0 < b_min <= b
+
+
+def test_status_needs_a_word():
+    """An empty view would have its flags set in its neighbour's memory."""
+    from lm_head_loss_junction_b200.api import _head_status
+    cpu, words = torch.device("cpu"), torch.zeros(4, dtype=torch.int32)
+    for good in (None, words, words[1:2], words[0]):
+        _head_status(good, cpu)
+    for bad, error in ((words[2:2], ValueError), (torch.zeros(0, dtype=torch.int32), ValueError)):
+        with pytest.raises(error):
+            _head_status(bad, cpu)

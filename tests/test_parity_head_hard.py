@@ -315,3 +315,20 @@ def test_rows_whose_sums_are_exact(D, T):
         within(stats[0], lse, off, kind + " lse")
         exp = np.take_along_axis(logq, ids, axis=1)
         within(logp, exp, (2 * off)[:, None] + 2.0 ** -22 * np.abs(exp), kind + " logp")
+
+
+# ---------------------------------------------------------------- refusals
+def test_empty_status_is_refused():
+    _, h, W, y = make(4, 64, 100, BF)
+    hg, Wg, yg = gpu(h, W, y)
+    ids, z = yg[:, None].contiguous(), torch.zeros(4, 1, device="cuda")
+    logp, stats, _, _ = token_logprobs(yg, hg, Wg)
+    _, dstats = topk_distill_fwd(yg, ids, z, hg, Wg)
+    words = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for status in (words[1:1], torch.zeros(0, dtype=torch.int32, device="cuda")):
+        for call in (lambda: token_logprobs(yg, hg, Wg, status=status),
+                     lambda: token_logprobs_bwd(yg, hg, Wg, stats, logp, status=status),
+                     lambda: topk_distill_fwd(yg, ids, z, hg, Wg, status=status),
+                     lambda: topk_distill_bwd(yg, ids, z, hg, Wg, dstats, status=status)):
+            with pytest.raises(ValueError):
+                call()
