@@ -538,7 +538,9 @@ mls_status mls_token_logprobs(int64_t T, int64_t D, int64_t V, int N, const int3
  * vocabulary at a time, each row over a power of two that brings the sum of its
  * coefficients' magnitudes to 2^14: an entry below 2^-28 of that sum has fewer
  * bits, one below 2^-39 of it is 0.  It is multiplied on the tensor cores with
- * fp16 copies of W and h, fp32 sums.
+ * fp16 copies of W and h, fp32 sums.  Values of W below 2^-27 of its largest have
+ * fewer bits in dh, those below 2^-38 of it none (so a vocabulary masked through a
+ * column of W needs its mask above -2^15), values of h likewise in dW.
  */
 mls_status mls_token_logprobs_bwd_workspace(int64_t T, int64_t D, int64_t V, int N, mls_dtype dt,
                                             size_t* bytes, size_t* min_bytes);

@@ -227,22 +227,36 @@ __global__ void __launch_bounds__(kThreads, 1) head_few_kernel(const __grid_cons
           }
 #pragma unroll
           for (int o = kSub / 2; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
-          if (cm > top) {
-            const float next = cm * a.log2e;
-            if (z > 0.f) {
-              const float d = m - next, f = ex2(d);
-              u = f * fmaf(d, z, u);
-              z *= f;
-            }
-            top = cm;
-            m = next;
-          }
+          if (fabsf(cm) > kLarge) {                        // the same for the threads of a token
+            const float low = fmaxf(cm, kLowest);
+            float cz = 0.f, cu = 0.f;
 #pragma unroll
-          for (int k = 0; k < kChunk; ++k) {
-            const float d = to_base2(l[k], a.log2e, m), x = ex2(d);
-            z += x;
-            u = fmaf(d, x, u);
+            for (int k = 0; k < kChunk; ++k) {
+              const float d = low_base2(l[k], a.log2e, low), x = ex2(d);
+              cz += x;
+              cu = fmaf(d, x, cu);
+            }
+            merge_part(m, z, u, low * a.log2e, cz, cu);
+            top = fmaxf(top, cm);
+          } else {
+            if (cm > top) {
+              const float next = cm * a.log2e;
+              if (z > 0.f) {
+                const float d = m - next, f = ex2(d);
+                u = f > 0.f ? f * fmaf(d, z, u) : 0.f;
+                z *= f;
+              }
+              top = cm;
+              m = next;
+            }
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) {
+              const float d = max_nan(to_base2(l[k], a.log2e, m), -200.f), x = ex2(d);
+              z += x;
+              u = fmaf(d, x, u);
+            }
           }
+          __syncwarp();
         }
 #pragma unroll
         for (int o = kSub / 2; o > 0; o >>= 1) {

@@ -245,27 +245,6 @@ __global__ void __launch_bounds__(256) head_exact_kernel(const HeadExact x, unsi
 }
 
 // ------------------------------------------------------------------ merge of partial statistics
-// (m, z, u) of two column sets -> of their union.
-__device__ __forceinline__ void merge_part(float& m, float& z, float& u, float m2, float z2, float u2) {
-  const float top = fmaxf(m, m2);
-  if (!(top > -INFINITY)) {                              // nothing on either side, or nothing that is a number
-    z += z2;
-    u += u2;
-    return;
-  }
-  if (z > 0.f || z != z) {
-    const float d = m - top, f = ex2(d);
-    u = f * fmaf(d, z, u);
-    z *= f;
-  }
-  if (z2 > 0.f || z2 != z2) {
-    const float d = m2 - top, f = ex2(d);
-    u = fmaf(f, fmaf(d, z2, u2), u);
-    z = fmaf(f, z2, z);
-  }
-  m = top;
-}
-
 __device__ __forceinline__ void warp_merge(float& m, float& z, float& u) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -346,8 +325,10 @@ __device__ __forceinline__ void refine_given(const HeadFinish& f, int64_t t, int
       dots64<BF16, 1>(h, f.W, f.D, id, lane, l);
       const float is = fine_base2(l[0], m);
       const float e0 = ex2(was), e1 = ex2(is);
-      z += e1 - e0;
-      u += is * e1 - was * e0;
+      if (fabsf(m) < kLarge) {         // else m stands for a logit (low_base2), and their logits have few bits after the point
+        z += e1 - e0;
+        u += is * e1 - was * e0;
+      }
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i)
         if (g.id[i] == id[0]) g.d[i] = is;
@@ -467,10 +448,11 @@ __global__ void __launch_bounds__(256) head_finish_rows_kernel(const HeadFinish 
   if (lane == 0) sm[warp] = top;
   __syncthreads();
   top = warp_max(lane < 8 ? sm[lane] : -INFINITY);
-  const float m = top * f.log2e;
+  const bool large = fabsf(top) > kLarge;
+  const float low = fmaxf(top, kLowest), m = (large ? low : top) * f.log2e;
   float z = 0.f, u = 0.f;
   for (int v = threadIdx.x; v < f.V; v += 256) {
-    const float d = to_base2(row[v], f.log2e, m), e = ex2(d);
+    const float d = large ? low_base2(row[v], f.log2e, low) : max_nan(to_base2(row[v], f.log2e, m), -200.f), e = ex2(d);
     z += e;
     u = fmaf(d, e, u);
   }
@@ -742,10 +724,10 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   largest = warp_max(lane < kWarps ? s.dz[lane] : -INFINITY);
   {
     // one reference for the block: that of the split with the largest logit
-    const float ref = largest * f.log2e;
+    const float ref = fmaxf(largest, kLowest) * f.log2e;
     if (z > 0.f || z != z) {
       const float d = m - ref, e = ex2(d);
-      u = e * fmaf(d, z, u);
+      u = e > 0.f ? e * fmaf(d, z, u) : 0.f;
       z *= e;
     }
     m = ref;
@@ -944,8 +926,9 @@ __global__ void __launch_bounds__(kTopThreads) head_top_kernel(const HeadFinish 
   if (r < have) {
     const float was = to_base2(s.tile[r], f.log2e, m), is = fine_base2(fine[r], m);
     const float e0 = ex2(was), e1 = ex2(is);
-    s.dz[rank] = e1 - e0;
-    s.du[rank] = is * e1 - was * e0;
+    const bool fix = fabsf(m) < kLarge;
+    s.dz[rank] = fix ? e1 - e0 : 0.f;
+    s.du[rank] = fix ? (e1 > 0.f ? is * e1 : 0.f) - (e0 > 0.f ? was * e0 : 0.f) : 0.f;
   }
   __syncthreads();
   if (warp * 32 >= kMaxEntries + kTopMore) return;

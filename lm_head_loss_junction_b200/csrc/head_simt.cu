@@ -153,11 +153,12 @@ __global__ void __launch_bounds__(256) split_stats_kernel(const float* logits, i
     top = fmaxf(top, l[k]);
   }
   top = warp_max(top);
-  const float m = top * kLog2e;
+  const bool large = fabsf(top) > kLarge;
+  const float low = fmaxf(top, kLowest), m = (large ? low : top) * kLog2e;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (c0 + k * 32 + lane >= V) continue;
-    const float d = to_base2(l[k], kLog2e, m), e = ex2(d);
+    const float d = large ? low_base2(l[k], kLog2e, low) : max_nan(to_base2(l[k], kLog2e, m), -200.f), e = ex2(d);
     z += e;
     u = fmaf(d, e, u);
   }
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(float* logits, int64_t l
   const float4 ri = en.row[t];
   for (int v = threadIdx.x; v < V; v += 256) {
     // the difference first: rounding lse log2(e) would cost every q of the row 1e-6 of itself
-    const float d = (row[v] - ri.x) * kLog2e;
+    const float d = max_nan((row[v] - ri.x) * kLog2e, -200.f);
     row[v] = ri.w == 0.f ? 0.f : ri.w * (ex2(d) * fmaf(ri.z * kLn2, d, ri.y));
   }
   __syncthreads();

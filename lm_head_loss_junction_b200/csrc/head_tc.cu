@@ -291,27 +291,43 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
 #pragma unroll
       for (int k = 4; k < 32; ++k) c4[k & 3] = fmaxf(c4[k & 3], r[k]);
       const float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
-      if (cm > top) {
-        // move the sums to the new reference: with d = m - m', a' = a + d, 2^a' = 2^d 2^a
-        const float next = cm * a.log2e;
-        if (z > 0.f) {
-          const float d = m - next, f = ex2(d);
-          u = f * fmaf(d, z, u);
-          z *= f;
+      if (fabsf(cm) > kLarge) {
+        // few instructions (they lie among the others'): from this lane's staged row
+        stage_row(s.stage[warp - 2], lane, r);
+        const float low = fmaxf(cm, kLowest);
+        float lz = 0.f, lu = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < 32; ++k) {
+          const float d = low_base2(*staged_at(s.stage[warp - 2], lane, k), a.log2e, low);
+          const float e = ex2(d);
+          lz += e;
+          lu = fmaf(d, e, lu);
         }
-        top = cm;
-        m = next;
-      }
-      float z4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
+        merge_part(m, z, u, low * a.log2e, lz, lu);
+        top = fmaxf(top, cm);
+      } else {
+        if (cm > top) {
+          // move the sums to the new reference: with d = m - m', a' = a + d, 2^a' = 2^d 2^a
+          const float next = cm * a.log2e;
+          if (z > 0.f) {
+            const float d = m - next, f = ex2(d);
+            u = f > 0.f ? f * fmaf(d, z, u) : 0.f;
+            z *= f;
+          }
+          top = cm;
+          m = next;
+        }
+        float z4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float d = to_base2(r[k], a.log2e, m);
-        const float e = ex2(d);
-        z4[k & 3] += e;
-        u4[k & 3] = fmaf(d, e, u4[k & 3]);
+        for (int k = 0; k < 32; ++k) {
+          const float d = max_nan(to_base2(r[k], a.log2e, m), -200.f);
+          const float e = ex2(d);
+          z4[k & 3] += e;
+          u4[k & 3] = fmaf(d, e, u4[k & 3]);
+        }
+        z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
+        u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
       }
-      z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
-      u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
       if constexpr (EPI == kLogits) {
         // through the staging rows: a store instruction writes 4 rows x 128 contiguous bytes
         uint8_t* stage = s.stage[warp - 2];
@@ -353,7 +369,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, TileSmem& s, uint32_
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const float d = to_base2(r[k], a.log2e, lse2);
-        r[k] = ex2(d) * fmaf(B2, d, A);
+        r[k] = ex2(d) * fmaf(B2, max_nan(d, -200.f), A);           // 2^-200 is 0 to ex2; d may be as low as a mask
       }
       if (!all_live || left < 32) {
 #pragma unroll

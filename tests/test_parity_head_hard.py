@@ -270,6 +270,43 @@ def test_more_logits_in_doubt_than_are_ranked_again():
         check_top(top, logp, h, W, K, Bounds(h, W))
 
 
+# ---------------------------------------------------------------- logits as low as a mask's
+def masked(T, D, V, dtype, value, seed=31):
+    """A column of h that is 1 and, in W, 0 or `value`: the vocabulary's entries that a program masks in this way."""
+    rng, h, W, y = make(T, D, V, dtype, seed=seed)
+    gone = np.zeros(V, dtype=bool)
+    gone[32:64] = gone[300:512] = gone[V - 50:] = True
+    gone[rng.choice(V, size=V // 10, replace=False)] = True
+    y = np.where(gone[y], np.flatnonzero(~gone)[rng.integers(0, (~gone).sum(), size=T)], y).astype(np.int32)
+    h[:, -1] = 1.0
+    W[:, -1] = torch.from_numpy(np.where(gone, value, 0.0).astype(np.float32)).to(dtype)
+    return rng, h, W, y, gone
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 60, 140])
+@pytest.mark.parametrize("value", [-1e4, -1e30, -1e37, float(torch.finfo(BF).min), -np.inf])
+def test_masked_vocabulary(dtype, T, value):
+    D, V, K = 64, 900, 20
+    rng, h, W, y, gone = masked(T, D, V, dtype, value)
+    hg, Wg, yg = gpu(h, W, y)
+    keep = np.flatnonzero(~gone)
+    at = np.searchsorted(keep, y)
+    small = W[torch.from_numpy(keep)]
+    b = Bounds(h, small)
+    r = oh.token_logprobs(at[:, None], h, small, top_k=K)
+    for k in (0, K):
+        logp, stats, top, tlp = token_logprobs(yg, hg, Wg, top_k=k)
+        within(stats[0], r["lse"], b.lse(r["lse"]), "lse")
+        within(stats[1], r["entropy"], b.entropy(r["entropy"]), "entropy")
+        within(logp[:, None], r["logp"], b.logp(r["lse"])[:, None], "logp")
+        if k:
+            np.testing.assert_array_equal(top.cpu().numpy(), keep[r["top_ids"]])
+    dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, torch.ones(T, device="cuda"), torch.full((T,), 0.1, device="cuda"))
+    assert not torch.isnan(dW).any()
+    assert not dW[torch.from_numpy(gone).cuda()].any()
+
+
 # ---------------------------------------------------------------- widths and exact rows
 @pytest.mark.parametrize("D", [2304, 4352])
 @pytest.mark.parametrize("T", [1, 70, 150])
