@@ -84,7 +84,8 @@ __device__ __forceinline__ void dots64(const void* h, const void* W, int64_t D, 
 template <bool BF16, typename Dense, typename Put>
 __device__ __forceinline__ void exact_entries(const int2* e, int begin, int end, const float4& ri, const void* h,
                                               const void* W, int64_t D, int lane, const Dense& dense, const Put& put) {
-  const float heavy = (fabsf(ri.y) + fabsf(ri.z)) * (1.f / 32);
+  const bool entropy = ri.z != 0.f;
+  const float heavy = fabsf(ri.y) * (1.f / 32);
   for (int i0 = begin; i0 < end; i0 += 32) {
     const int i = i0 + lane;
     int own = 0;
@@ -95,12 +96,13 @@ __device__ __forceinline__ void exact_entries(const int2* e, int begin, int end,
       once = i == begin || e[i - 1].x != own;
       if (once) {
         for (int j = i; j < end && e[j].x == own; ++j) sum += __int_as_float(e[j].y);
-        // a coefficient that is small beside the row leaves no small difference there
-        some = fabsf(sum) > 0.5f * heavy;
+        // a coefficient that is small beside the row leaves no small difference there; with an entropy's gradient,
+        // q (A + B log q) is one itself
+        some = entropy || fabsf(sum) > 0.5f * heavy;
         if (some || !BF16) was = dense(own, sum);
       }
     }
-    const bool again = some && fabsf(was) > heavy;
+    const bool again = entropy ? some : some && fabsf(was) > heavy;
     if (once && !again) put(own, was + sum, false);
     unsigned todo = __ballot_sync(0xffffffffu, again);
     while (todo != 0) {

@@ -143,6 +143,56 @@ def test_heavy_entries_named_twice():
     check_grads(b, d["G"], np.full(T, 1.0 / T), *topk_distill_bwd(yg, ig, gpu(z)[0], hg, Wg, dstats, 0.4))
 
 
+@pytest.mark.parametrize("T", [40, 150])
+@pytest.mark.parametrize("D", [640, 4352])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("top_k", [0, 8])
+def test_peaked_rows_whose_sums_are_exact(T, D, dtype, top_k):
+    """One entry a row in h, the target at 64 and every other token at 46 or 45: no sum is truncated, so a tensor-core
+    logit is off by what is given back, dl = D 2^-30 of it, and nothing else (fp32: not at all).  Gradients of the log
+    probability, and of the entropy, whose own difference is that of log q_y and minus the entropy.
+
+    Bound of an entry of G = s (g (1_y - q) - e q (log q + H)), with z = sum e^(l - l_y) near 1: after the target's term
+    come up to 64 of its block of columns (a thread's share of 128, 40 tokens) and 16 merges, each rounding z by 2^-24:
+    2^-17.6, and so much of its logarithm, in log-sum-exp and entropy.  The log-sum-exp is rounded to fp32 (2^-24 |lse|);
+    the others' part of the entropy is off by 2 dl, their logits and log-sum-exp by 2 dl of themselves.  fp16: 2^-11, and
+    2^-36 s below its range (the row's bound is at most 9 s)."""
+    V, s = 5000, 1.0 / T
+    rng = np.random.Generator(np.random.PCG64(28))
+    y = rng.choice(V, size=T, replace=False).astype(np.int32)
+    h = torch.zeros(T, D)
+    h[:, 0] = 32.0
+    W = torch.from_numpy(rng.integers(0, 9, size=(V, D)) / 4.0).float()
+    W[:, 0] = torch.from_numpy(np.where(rng.random(V) < 0.5, 46.0, 45.0) / 32).float()
+    # each token its own head column, so that only its target is large
+    own = 1 + np.arange(T)
+    h[torch.arange(T), torch.from_numpy(own)] = 8.0
+    W[:, 1:T + 1] = 0.0
+    W[torch.from_numpy(y.astype(np.int64)), torch.from_numpy(own)] = (64.0 - 32 * W[torch.from_numpy(y.astype(np.int64)), 0]) / 8
+    h, W = h.to(dtype), W.to(dtype)
+    b = Bounds(h, W)
+    rows = np.arange(T)
+    logq, lse = oh.log_softmax(b.h @ b.W.T)
+    q = np.exp(logq)
+    assert (np.abs(b.h @ b.W.T)[rows, y] == 64).all() and 0.9998 < q[rows, y].min() and q[rows, y].max() < 0.99999
+    H = -np.sum(q * logq, axis=1)
+    hg, Wg, yg = gpu(h, W, y)
+    _, stats, _, _ = token_logprobs(yg, hg, Wg, top_k=top_k)
+    dl = D * 2.0 ** -30 * 64 if b.bf16 else 0.0
+    eH = 2 * dl * 20 * (1 - q[rows, y]) + 2.0 ** -17.6
+    elq = 2.0 ** -24 * np.abs(lse) + 2.0 ** -17.6
+    within(stats[1], H, eH, "entropy")
+    for g, e in ((s, 0.0), (0.0, s), (s, 0.01 * s)):
+        G = oh.token_logprobs_grad(y[:, None], b.h, b.W, np.full((T, 1), g), np.full(T, e))
+        off = q * (g * (2 * dl + 2.0 ** -19) + e * (2 * dl * (np.abs(logq) + 1) + 2.0 ** -19 * (1 + np.abs(logq)) + eH[:, None]))
+        off[rows, y] = g * elq + e * (elq + eH)
+        off += 2.0 ** -11 * np.abs(G) + 2.0 ** -36 * s if b.bf16 else 2.0 ** -22 * np.abs(G)
+        dh, dW = token_logprobs_bwd(yg, hg, Wg, stats, torch.full((T,), g, device="cuda"),
+                                    torch.full((T,), e, device="cuda") if e else None)
+        exp = G @ b.W
+        within(dh, exp, off @ np.abs(b.W) + b._sum(V) * (np.abs(G) @ np.abs(b.W)) + half_step(dh.dtype) * np.abs(exp), "dh")
+
+
 # ---------------------------------------------------------------- magnitudes
 class Tiny(Bounds):
     """With what is lost below the smallest normal number: half of the output's smallest number, and of fp32's for
