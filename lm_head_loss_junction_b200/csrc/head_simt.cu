@@ -1,7 +1,7 @@
 // fp32 path of the single-exit LM-head operators: CUDA-core matrix products
 // (tensor cores would round fp32 inputs), logits of a block of tokens in the
 // workspace, any sizes.  For the small single-precision suite; bound by
-// latency there (a handful of 64 x 64 tiles).
+// latency there (one tile of 16 x 16 or 32 x 32 per SM).
 #include "head.h"
 #include "head_dev.cuh"
 #include "head_exact.cuh"

@@ -13,8 +13,8 @@
 //   dh      G' W (K = columns of the chunk), scaled per row
 //   dw      G'^T h (K = tokens)
 // All five are bound by the tensor pipe once T passes a few hundred tokens (dh
-// and dw at 1.38 and 1.41 PFLOP/s, stats at 1.30, grad at 1.20 with T = 2048,
-// D = 1024, V = 49152; in long runs by the power cap, at the rate of cuBLAS's
+// and dw at 1.36 and 1.39 PFLOP/s, stats at 1.27, grad at 1.20 with T = 2048,
+// D = 1024, V = 49152; in long runs by the power cap, within 4% of cuBLAS's
 // products of the same shapes), and by reading W and a launch's own start and
 // tail below that.
 //
