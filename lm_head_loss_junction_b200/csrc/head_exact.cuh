@@ -112,7 +112,8 @@ __device__ __forceinline__ void exact_entries(const int2* e, int begin, int end,
       double l[1];
       dots64<BF16, 1>(h, W, D, id, lane, l);
       if (lane == src) {
-        const float d = static_cast<float>((l[0] - static_cast<double>(ri.x)) * 1.4426950408889634);
+        // (2^-200 is 0 to ex2; a masked token's d may be infinite)
+        const float d = max_nan(static_cast<float>((l[0] - static_cast<double>(ri.x)) * 1.4426950408889634), -200.f);
         put(own, fmaf(ex2(d), fmaf(ri.z * kLn2, d, ri.y), sum), true);
       }
     }

@@ -357,6 +357,38 @@ def test_masked_vocabulary(dtype, T, value):
     assert not dW[torch.from_numpy(gone).cuda()].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 60, 140])
+@pytest.mark.parametrize("value", [-1e4, -1e37, float(torch.finfo(BF).min), -np.inf])
+def test_masked_tokens_named(dtype, T, value):
+    """A masked token among the given ones: no probability, so its entry of the gradient is its coefficient, with an
+    entropy's gradient too."""
+    rng, h, W, y, gone = masked(T, 64, 900, dtype, value)
+    keep = np.flatnonzero(~gone)
+    at = np.searchsorted(keep, y)
+    small = W[torch.from_numpy(keep)]
+    out = np.flatnonzero(gone)[rng.integers(0, gone.sum(), size=T)].astype(np.int32)
+    ids = np.stack([y, out], axis=1)
+    g = rng.normal(size=(T, 2)).astype(np.float32)
+    e = np.full(T, 0.1, dtype=np.float32)
+    hg, Wg, ig, gg, eg = gpu(h, W, ids, g, e)
+    logp, stats, _, _ = token_logprobs(ig, hg, Wg)
+    assert (logp[:, 1] < -9e3).all()
+    b = Bounds(h, small)
+    G = oh.token_logprobs_grad(at[:, None], h, small, g[:, :1], e)
+    G -= np.exp(oh.log_softmax(b.h @ b.W.T)[0]) * g[:, 1:].astype(np.float64)
+    s = np.maximum(np.abs(g).max(1), np.abs(g.astype(np.float64).sum(1)))
+    _, dW = token_logprobs_bwd(ig, hg, Wg, stats, gg, eg)
+    check_grads(b, G, s, None, dW[torch.from_numpy(keep).cuda()])
+    exp = np.zeros(W.shape)
+    np.add.at(exp, out, g[:, 1:].astype(np.float64) * b.h)
+    size = np.zeros(W.shape)
+    np.add.at(size, out, np.abs(g[:, 1:].astype(np.float64) * b.h))
+    # the coefficient in fp16, h's copy, the sums
+    within(dW[torch.from_numpy(gone).cuda()], exp[gone], (size * (2.0 ** -11 + 2.0 ** -24 + b._sum(T)))[gone] +
+           2.0 ** -37 * s.max() * np.abs(b.h).max() * T, "dW of masked tokens")
+
+
 # ---------------------------------------------------------------- widths and exact rows
 @pytest.mark.parametrize("D", [2304, 4352])
 @pytest.mark.parametrize("T", [1, 70, 150])
