@@ -485,8 +485,8 @@ mls_status mls_exit_agreement(int M, int64_t T, int64_t V, const int64_t* D,
  *              to call; two calls that may overlap on the GPU (two captured
  *              graphs among them) need one each.
  * MLS_BF16 logits are fp32 sums of the tensor cores, which truncate; the mean of
- * what that takes is given back, D 2^-30 of a logit and at most 4352 2^-30.  Rows
- * whose sums need no truncation are off by so much.  Given tokens and targets with
+ * what that takes (measured for D up to 65536) is given back, D 2^-30 of a logit.
+ * Rows whose sums need no truncation are off by so much.  Given tokens and targets with
  * more than 1/16 of their row, and the alternatives, have logits summed in 64 bits.
  * Results are deterministic (no floating-point atomics); dh and dW may differ in
  * the last bits between workspace sizes, the other results do not.

@@ -35,18 +35,16 @@ typedef float4 HeadPart;
 
 // log2(e) for logits of the tensor cores.  Each of the D / 16 steps of an
 // accumulation truncates the running sum, which shrinks a logit: measured
-// against 64 bits, by 0.21 to 0.27 x 2^-24 of itself per step for D from 512 to
-// 4352, logits of random rows and of a leant-to row alike.  A quarter of 2^-24
-// per step is given back here (D = 2304: the mean error of a logit falls from
-// 2.1e-6 to under 0.2e-6 of it, the root mean square from 4.8e-6 to 2.4e-6;
-// plain fp32 sums have 0.9e-6).  A row whose sums are exact (a few entries, small
-// whole numbers) was not shrunk and is off by what is given back, so no more is
-// given than was measured: 4352 2^-30 = 4.1e-6 of a logit at most, whatever D.
-// parts: accumulators that share the steps.
-constexpr int64_t kTruncationMeasured = 4352;
+// against 64 bits, by 0.20 to 0.28 x 2^-24 of itself per step for every D from
+// 512 to 65536, logits of random rows, of a leant-to row and of heads with a mean
+// row alike (0.26 to 0.27 from D = 8192 on).  A quarter of 2^-24 per step is given
+// back here (D = 2304: the mean error of a logit falls from 2.1e-6 to under 0.2e-6
+// of it, the root mean square from 4.8e-6 to 2.4e-6; plain fp32 sums have 0.9e-6.
+// D = 65536, a leant-to row: 6.6e-5 to 0.6e-5).  A row whose sums are exact (a few
+// entries, small whole numbers) was not shrunk and is off by what is given back,
+// D 2^-30.  parts: accumulators that share the steps.
 inline float head_log2e(int64_t D, int parts) {
-  const int64_t d = D / parts < kTruncationMeasured ? D / parts : kTruncationMeasured;
-  return static_cast<float>(1.4426950408889634 * (1.0 + static_cast<double>(d) / 1073741824.0));
+  return static_cast<float>(1.4426950408889634 * (1.0 + static_cast<double>(D) / parts / 1073741824.0));
 }
 
 struct HeadProblem {

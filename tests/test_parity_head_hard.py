@@ -390,7 +390,7 @@ def test_masked_tokens_named(dtype, T, value):
 
 
 # ---------------------------------------------------------------- widths and exact rows
-@pytest.mark.parametrize("D", [2304, 4352])
+@pytest.mark.parametrize("D", [2304, 4352, 8192])
 @pytest.mark.parametrize("T", [1, 70, 150])
 def test_the_widths_of_the_larger_exits(D, T):
     rng, h, W, y = make(T, D, 2000, BF, seed=24)
@@ -412,8 +412,8 @@ def test_the_widths_of_the_larger_exits(D, T):
 @pytest.mark.parametrize("T", [1, 128, 129])
 def test_rows_whose_sums_are_exact(D, T):
     """h with one entry a row, and h and W of small whole numbers: no addition rounds or truncates, so what is left
-    is the correction for truncation that did not happen: at most min(D, 4352) 2^-30 of a logit (the fp32 log-sum-exp and
-    the exponentials: 2^-20 as everywhere)."""
+    is the correction for truncation that did not happen: D 2^-30 of a logit (the fp32 log-sum-exp and the exponentials:
+    2^-20 as everywhere)."""
     rng = np.random.Generator(np.random.PCG64(25))
     V = 300
     for kind in ("one", "whole"):
@@ -430,7 +430,7 @@ def test_rows_whose_sums_are_exact(D, T):
         ids = np.argsort(-l, axis=1, kind="stable")[:, [0, V // 2]].astype(np.int32)
         hg, Wg, ig = gpu(h, W, ids)
         logp, stats, _, _ = token_logprobs(ig, hg, Wg)
-        off = min(D, 4352) * 2.0 ** -30 * np.abs(l).max(axis=1) + 2.0 ** -20 * (1 + np.abs(lse))
+        off = D * 2.0 ** -30 * np.abs(l).max(axis=1) + 2.0 ** -20 * (1 + np.abs(lse))
         within(stats[0], lse, off, kind + " lse")
         exp = np.take_along_axis(logq, ids, axis=1)
         within(logp, exp, (2 * off)[:, None] + 2.0 ** -22 * np.abs(exp), kind + " logp")
